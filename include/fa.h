@@ -379,6 +379,109 @@ FA_API int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, v
                            int B, int H, int N_q, int N_k, int d, float scale, int causal,
                            const int32_t *key_lens, int num_splits, fa_stream_t stream);
 
+/*
+ * A paged key/value cache held in 4 bits.
+ *
+ * Serving keeps the keys and values of all earlier tokens; a decoding step reads them
+ * once per new token and is bound by those bytes ("FlashAttention：把注意力从公式写成数据流",
+ * sections "端侧与专用加速器" and "FA2 与 FA3" name the decode case and low-precision
+ * storage; the paper has no 4-bit form, so the format is this library's own).  Three
+ * operators share one cache: fa_kv4_append quantises new tokens as it writes them,
+ * fa_kv4_read gives a span back as dense bf16, and fa_fwd_kv4 attends over the cache
+ * without ever forming a 16-bit copy of it.
+ *
+ * Layout (K and V each have one of both buffers):
+ *   codes   uint8 [num_pages, H_kv, page_size, d/2]: byte i of a token's row holds the code
+ *           of channel 2i in its low half, of channel 2i+1 in its high half;
+ *   scales  bf16 [num_pages, H_kv, page_size, d/32]: one per group of 32 channels.
+ * With m the group's value of largest magnitude (the positive one of an equal pair):
+ *   s = -m/8, rounded to 5 significant bits (ties to even),
+ *   c = clamp(rint(x/s), -8, 7) + 8 (ties to even),  and c stands for (c - 8) * s,
+ * which is exactly a bf16 number, |s|/2 from x at most, or 1.25 |s| next to -m, for which
+ * there is no code (0.56 bytes an element instead of 2).  A group that holds a value that is not finite, or above 2^120 in
+ * magnitude, stands for NaN; one whose values are all below 2^-107 stands for zeros.
+ *
+ * Sequences and pages:
+ *   block_table  device int32 [B, max_pages]: the pages of each sequence in order; NULL:
+ *                page p of sequence b is b * max_pages + p (a dense cache is page_size =
+ *                its capacity, max_pages = 1, num_pages = B).  A number outside
+ *                [0, num_pages) names no page: nothing is written for its positions, they
+ *                read back as zeros and are masked in the attention.  Two sequences may
+ *                share pages that neither writes.
+ *   key_lens     device int32 [B], required: tokens of each sequence INCLUDING those that
+ *                the call appends or queries; clamped to [0, max_pages * page_size] by
+ *                fa_kv4_read and fa_fwd_kv4.
+ *   page_size    > 0, a multiple of 16; max_pages * page_size <= 2^30.
+ * Codes and scales are 16-byte aligned, k, v, q and o 16-byte, int32 arrays and lse 4-byte.
+ * d is 64 or 128.  All calls are asynchronous on `stream` and run on the current device,
+ * which must own the buffers; the library allocates nothing.
+ */
+
+/*
+ * fa_kv4_append -- quantise new tokens and write them to the cache.
+ *
+ *   k, v       device bf16 [B, H_kv, N_new, d].
+ *   new_lens   NULL (all N_new), or device int32 [B]: sequence b has min(new_lens[b], N_new)
+ *              new tokens (the rest of its rows is padding and is not read).
+ * Token n of sequence b is written to position key_lens[b] - new_b + n; a position below 0
+ * or past the sequence's pages is skipped.  Nothing else in the cache changes.  No two
+ * tokens of a call may have the same place (sequences that write a shared page): which
+ * one the place then holds is not defined.
+ * Returns FA_OK once enqueued; FA_ERR_INVALID_ARG / FA_ERR_UNSUPPORTED /
+ * FA_ERR_MISALIGNED for bad arguments (before any CUDA call), FA_ERR_NO_DEVICE or
+ * FA_ERR_CUDA otherwise.  B, H_kv or N_new equal to 0 is a no-op.
+ */
+FA_API int fa_kv4_append(const void *k, const void *v, void *k_codes, void *k_scales,
+                         void *v_codes, void *v_scales, const int32_t *block_table,
+                         const int32_t *key_lens, const int32_t *new_lens, int B, int H_kv,
+                         int N_new, int d, int num_pages, int page_size, int max_pages,
+                         fa_stream_t stream);
+
+/*
+ * fa_kv4_read -- the values that a span of the cache stands for, as dense bf16 in the
+ * layout of fa_fwd (so that fa_fwd, or any other entry point, can attend over them).
+ *
+ *   first   NULL (0), or device int32 [B]: the first position to read of each sequence.
+ *   k, v    device bf16 [B, H_kv, N, d], written in full: row n of sequence b holds
+ *           position first[b] + n, and zeros where that is outside [0, key_lens[b]).
+ * Returns as fa_kv4_append.  Exact: nothing is rounded.
+ */
+FA_API int fa_kv4_read(const void *k_codes, const void *k_scales, const void *v_codes,
+                       const void *v_scales, const int32_t *block_table,
+                       const int32_t *key_lens, const int32_t *first, void *k, void *v, int B,
+                       int H_kv, int N, int d, int num_pages, int page_size, int max_pages,
+                       fa_stream_t stream);
+
+/*
+ * fa_fwd_kv4 -- attention over the cache: O = softmax(scale * Q K^T + mask) V and its LSE
+ * (as fa_fwd), with K and V the values that the codes stand for.
+ *
+ *   q          device bf16 [B, H, N_q, d].  H is a multiple of H_kv: query head h attends
+ *              to key/value head h / (H / H_kv).
+ *   q_lens     NULL (all N_q), or device int32 [B]: queries of each sequence, clamped to
+ *              [0, N_q].  Query i of sequence b stands at position key_lens[b] - q_b + i.
+ *   o, lse     device bf16 [B, H, N_q, d] and fp32 [B, H, N_q], written in full; a query
+ *              that sees no key, or is past its sequence's queries, gets O = +0, LSE = -inf.
+ *   causal     non-zero: a query sees no key after its own position.
+ *   window_left  < 0: no window; >= 0: a query sees no key more than window_left before
+ *              its own position.
+ *   workspace  device, 256-byte aligned, at least fa_fwd_kv4_workspace_size(B, H, H_kv,
+ *              N_q, d) bytes, owned by the caller; needs no initial contents.  Calls that
+ *              share a workspace must be ordered (one stream, or events); captured calls
+ *              may be replayed, and graphs that are ordered may share one.
+ * K and V of a key that a query does not see have no influence on it, whatever they hold.
+ * For a given device the result depends on the arguments alone, bit for bit.
+ * Returns as fa_fwd; FA_ERR_INVALID_ARG also for H not a multiple of H_kv, a NULL or short
+ * workspace.  B, H or N_q equal to 0 is a no-op.
+ */
+FA_API size_t fa_fwd_kv4_workspace_size(int B, int H, int H_kv, int N_q, int d);
+FA_API int fa_fwd_kv4(const void *q, const void *k_codes, const void *k_scales,
+                      const void *v_codes, const void *v_scales, const int32_t *block_table,
+                      const int32_t *key_lens, const int32_t *q_lens, void *o, float *lse, int B,
+                      int H, int H_kv, int N_q, int d, int num_pages, int page_size,
+                      int max_pages, float scale, int causal, int window_left, void *workspace,
+                      size_t workspace_bytes, fa_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 FA_API const char *fa_status_string(int status);
 

@@ -90,6 +90,14 @@ def load_library() -> ctypes.CDLL:
             lib.fa_fwd_splitkv_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                                    f32, i32, vp, i32, vp]
             lib.fa_fwd_splitkv_noalloc.restype = i32
+            lib.fa_kv4_append.argtypes = [vp] * 9 + [i32] * 7 + [vp]
+            lib.fa_kv4_append.restype = i32
+            lib.fa_kv4_read.argtypes = [vp] * 9 + [i32] * 7 + [vp]
+            lib.fa_kv4_read.restype = i32
+            lib.fa_fwd_kv4_workspace_size.argtypes = [i32] * 5
+            lib.fa_fwd_kv4_workspace_size.restype = sz
+            lib.fa_fwd_kv4.argtypes = [vp] * 10 + [i32] * 8 + [f32, i32, i32, vp, sz, vp]
+            lib.fa_fwd_kv4.restype = i32
             lib.fa_status_string.argtypes = [i32]
             lib.fa_status_string.restype = ctypes.c_char_p
             lib.fa_get_device_status.argtypes = [vp]
@@ -262,6 +270,53 @@ def fa_fwd_splitkv_noalloc(q, k, v, o, lse, B, H, N_q, N_k, d, scale, causal, ke
                                                int(num_splits), _stream(stream))
     if check and st != FA_OK:
         raise FaError(st, "fa_fwd_splitkv_noalloc")
+    return st
+
+
+def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, new_lens, B,
+                  H_kv, N_new, d, num_pages, page_size, max_pages, stream=None, check=True) -> int:
+    """``fa_kv4_append`` of include/fa.h: quantise new tokens into the 4-bit paged cache."""
+    st = load_library().fa_kv4_append(_addr(k), _addr(v), _addr(k_codes), _addr(k_scales),
+                                      _addr(v_codes), _addr(v_scales), _addr(block_table),
+                                      _addr(key_lens), _addr(new_lens), int(B), int(H_kv),
+                                      int(N_new), int(d), int(num_pages), int(page_size),
+                                      int(max_pages), _stream(stream))
+    if check and st != FA_OK:
+        raise FaError(st, "fa_kv4_append")
+    return st
+
+
+def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, first, k, v, B, H_kv,
+                N, d, num_pages, page_size, max_pages, stream=None, check=True) -> int:
+    """``fa_kv4_read`` of include/fa.h: a span of the 4-bit cache as dense bf16."""
+    st = load_library().fa_kv4_read(_addr(k_codes), _addr(k_scales), _addr(v_codes),
+                                    _addr(v_scales), _addr(block_table), _addr(key_lens),
+                                    _addr(first), _addr(k), _addr(v), int(B), int(H_kv), int(N),
+                                    int(d), int(num_pages), int(page_size), int(max_pages),
+                                    _stream(stream))
+    if check and st != FA_OK:
+        raise FaError(st, "fa_kv4_read")
+    return st
+
+
+def fa_fwd_kv4_workspace_size(B, H, H_kv, N_q, d) -> int:
+    return int(load_library().fa_fwd_kv4_workspace_size(int(B), int(H), int(H_kv), int(N_q),
+                                                        int(d)))
+
+
+def fa_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o, lse, B,
+               H, H_kv, N_q, d, num_pages, page_size, max_pages, scale, causal, window_left,
+               workspace, workspace_bytes, stream=None, check=True) -> int:
+    """``fa_fwd_kv4`` of include/fa.h: attention over the 4-bit paged cache."""
+    st = load_library().fa_fwd_kv4(_addr(q), _addr(k_codes), _addr(k_scales), _addr(v_codes),
+                                   _addr(v_scales), _addr(block_table), _addr(key_lens),
+                                   _addr(q_lens), _addr(o), _addr(lse), int(B), int(H), int(H_kv),
+                                   int(N_q), int(d), int(num_pages), int(page_size),
+                                   int(max_pages), float(scale), int(bool(causal)),
+                                   int(window_left), _addr(workspace), int(workspace_bytes),
+                                   _stream(stream))
+    if check and st != FA_OK:
+        raise FaError(st, "fa_fwd_kv4")
     return st
 
 

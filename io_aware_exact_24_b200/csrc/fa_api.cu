@@ -19,6 +19,7 @@
 #include <utility>
 
 #include "fa.h"
+#include "fa_internal.h"
 #include "fa_bwd_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd_persist.cuh"
@@ -577,6 +578,27 @@ __global__ void selftest_wait_kernel(unsigned long long limit) {
 }
 
 }  // namespace
+
+namespace fa_internal {
+
+int cuda_fail(const char* what, cudaError_t e) { return ::cuda_fail(what, e); }
+
+int ready_device(int* dev, int* num_sms) {
+    int ndev = 0;
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
+        cudaGetLastError();
+        return FA_ERR_NO_DEVICE;
+    }
+    const cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return ::cuda_fail("cudaGetDevice", e);
+    const int st = prepare_device(*dev);
+    if (st == FA_OK) *num_sms = g_dev[*dev].num_sms;
+    return st;
+}
+
+int current_num_sms() { return ::current_num_sms(); }
+
+}  // namespace fa_internal
 
 extern "C" {
 

@@ -1,0 +1,270 @@
+// fa_kv4.cu -- host side of the 4-bit paged key/value cache entry points (include/fa.h):
+// argument checks (before any CUDA call), workspace layout and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <chrono>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "fa.h"
+#include "fa_internal.h"
+#include "fa_kv4_attend.cuh"
+#include "fa_kv4_kernel.cuh"
+
+namespace {
+
+using fa_internal::cuda_fail;
+using fa_internal::ready_device;
+namespace kv4 = fa::kv4;
+
+constexpr int kMaxPositions = 1 << 30;   // max_pages * page_size: positions and tile numbers stay within int
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Checks that the three entry points share; *empty: nothing to do.
+int validate(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+             const int32_t* block_table, const int32_t* key_lens, const int32_t* lens, int B, int H_kv, int N, int d,
+             int num_pages, int page_size, int max_pages, bool* empty) {
+    if (B < 0 || H_kv < 0 || N < 0 || num_pages < 0 || max_pages < 0 || page_size <= 0) return FA_ERR_INVALID_ARG;
+    if (page_size % 16 != 0) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > kMaxPositions) return FA_ERR_UNSUPPORTED;
+    *empty = B == 0 || H_kv == 0 || N == 0;
+    if (*empty) return FA_OK;
+    if (B > 65535 || H_kv > 65535) return FA_ERR_UNSUPPORTED;
+    if (key_lens == nullptr) return FA_ERR_INVALID_ARG;
+    if (num_pages > 0 &&
+        (k_codes == nullptr || k_scales == nullptr || v_codes == nullptr || v_scales == nullptr))
+        return FA_ERR_INVALID_ARG;
+    for (const void* p : {k_codes, k_scales, v_codes, v_scales})
+        if (!aligned(p, 16)) return FA_ERR_MISALIGNED;
+    for (const int32_t* p : {block_table, key_lens, lens})
+        if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+kv4::Paging paging(const int32_t* table, int num_pages, int page_size, int max_pages) {
+    kv4::Paging pg;
+    pg.table = table;
+    pg.num_pages = num_pages;
+    pg.page_size = page_size;
+    pg.max_pages = max_pages;
+    pg.magic = 0xffffffffu / (uint32_t)page_size;
+    return pg;
+}
+
+// Grid of one thread per 8 channels of `rows` rows; false if it exceeds the launch limits.
+bool row_grid(long long rows, int d, unsigned* blocks) {
+    const long long per = 256 / (d / 8), n = (rows + per - 1) / per;
+    *blocks = (unsigned)n;
+    return n <= 0x7fffffffLL;
+}
+
+// A 48-bit ticket other than 0 for each attention launch (see kv4::arrive_last).
+unsigned long long next_ticket() {
+    static std::atomic<unsigned long long> seq{
+        (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15ull};
+    unsigned long long t = 0;
+    while (t == 0) t = (seq.fetch_add(1, std::memory_order_relaxed) + 1) & ((1ull << 48) - 1);
+    return t;
+}
+
+// Rows per block: one MMA column block holds 8 query rows.
+int row_block(long long R) { return R <= 8 ? 8 : 16; }
+int ctas_per_sm(int rb) { return rb == 8 ? 2 : 1; }
+
+// Workspace of the attention: two partial results per CTA, then the arrival words.
+struct Layout {
+    size_t part, ml, words, total;
+};
+Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
+    const long long R = (long long)(H / H_kv) * N_q;
+    const int rb = row_block(R);
+    const size_t slots = 2 * (size_t)num_sms * ctas_per_sm(rb);
+    const long long entries = (R + rb - 1) / rb * B;
+    Layout L{};
+    L.part = 0;
+    L.ml = round_up(slots * rb * d * 4);
+    L.words = L.ml + round_up(slots * rb * 16);
+    L.total = L.words + round_up((size_t)std::min<long long>(entries, kv4::kMaxEntries) * H_kv * 8);
+    return L;
+}
+
+std::once_flag g_once[64];
+int g_status[64];
+
+template <int D, int NB>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(kv4::attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kv4::Cfg<D, NB>::kSmemBytes);
+}
+int prepare_attend(int dev) {
+    std::call_once(g_once[dev], [&] {
+        cudaError_t e = set_smem<64, 1>();
+        if (e == cudaSuccess) e = set_smem<64, 2>();
+        if (e == cudaSuccess) e = set_smem<128, 1>();
+        if (e == cudaSuccess) e = set_smem<128, 2>();
+        g_status[dev] = e == cudaSuccess ? FA_OK : cuda_fail("cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", e);
+    });
+    return g_status[dev];
+}
+
+template <int D, int NB>
+void launch_attend(const kv4::AttendParams& p, int num_sms, cudaStream_t s) {
+    const int grid = num_sms * ctas_per_sm(8 * NB);
+    kv4::attend_kernel<D, NB><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                  const int32_t* block_table, const int32_t* key_lens, const int32_t* new_lens, int B, int H_kv,
+                  int N_new, int d, int num_pages, int page_size, int max_pages, fa_stream_t stream) {
+    bool empty = false;
+    int st = validate(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, new_lens, B, H_kv, N_new, d,
+                      num_pages, page_size, max_pages, &empty);
+    if (st != FA_OK || empty) return st;
+    if (k == nullptr || v == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16)) return FA_ERR_MISALIGNED;
+    kv4::AppendParams p{};
+    p.k = static_cast<const uint4*>(k);
+    p.v = static_cast<const uint4*>(v);
+    p.k_codes = static_cast<uint32_t*>(k_codes);
+    p.k_scales = static_cast<uint16_t*>(k_scales);
+    p.v_codes = static_cast<uint32_t*>(v_codes);
+    p.v_scales = static_cast<uint16_t*>(v_scales);
+    p.key_lens = key_lens;
+    p.new_lens = new_lens;
+    p.pg = paging(block_table, num_pages, page_size, max_pages);
+    p.H_kv = H_kv;
+    p.N = N_new;
+    p.rows = (long long)B * H_kv * N_new;
+    unsigned blocks = 0;
+    if (!row_grid(p.rows, d, &blocks)) return FA_ERR_UNSUPPORTED;
+    int dev = -1, sms = 0;
+    st = ready_device(&dev, &sms);
+    if (st != FA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d == 64)
+        kv4::append_kernel<64><<<blocks, 256, 0, s>>>(p);
+    else
+        kv4::append_kernel<128><<<blocks, 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache append)", e);
+}
+
+int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                const int32_t* block_table, const int32_t* key_lens, const int32_t* first, void* k, void* v, int B,
+                int H_kv, int N, int d, int num_pages, int page_size, int max_pages, fa_stream_t stream) {
+    bool empty = false;
+    int st = validate(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, first, B, H_kv, N, d, num_pages,
+                      page_size, max_pages, &empty);
+    if (st != FA_OK || empty) return st;
+    if (k == nullptr || v == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16)) return FA_ERR_MISALIGNED;
+    kv4::ReadParams p{};
+    p.k_codes = static_cast<const uint32_t*>(k_codes);
+    p.k_scales = static_cast<const uint16_t*>(k_scales);
+    p.v_codes = static_cast<const uint32_t*>(v_codes);
+    p.v_scales = static_cast<const uint16_t*>(v_scales);
+    p.key_lens = key_lens;
+    p.first = first;
+    p.k = static_cast<uint4*>(k);
+    p.v = static_cast<uint4*>(v);
+    p.pg = paging(block_table, num_pages, page_size, max_pages);
+    p.H_kv = H_kv;
+    p.N = N;
+    p.rows = (long long)B * H_kv * N;
+    unsigned blocks = 0;
+    if (!row_grid(p.rows, d, &blocks)) return FA_ERR_UNSUPPORTED;
+    int dev = -1, sms = 0;
+    st = ready_device(&dev, &sms);
+    if (st != FA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d == 64)
+        kv4::read_kernel<64><<<blocks, 256, 0, s>>>(p);
+    else
+        kv4::read_kernel<128><<<blocks, 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache read)", e);
+}
+
+size_t fa_fwd_kv4_workspace_size(int B, int H, int H_kv, int N_q, int d) {
+    if (B <= 0 || H <= 0 || H_kv <= 0 || N_q <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+    if (B > 65535 || H > 65535) return 0;
+    return layout(B, H, H_kv, N_q, d, fa_internal::current_num_sms()).total;
+}
+
+int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+               const int32_t* block_table, const int32_t* key_lens, const int32_t* q_lens, void* o, float* lse, int B,
+               int H, int H_kv, int N_q, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
+               int window_left, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    bool empty = false;
+    int st = validate(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, B, H_kv, N_q, d, num_pages,
+                      page_size, max_pages, &empty);
+    if (st != FA_OK) return st;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(scale) || !(scale > 0.f) || !(scale_log2 > 0.f) || !std::isfinite(scale_log2))
+        return FA_ERR_INVALID_ARG;
+    if (H < 0 || (H_kv > 0 && H % H_kv != 0) || (H_kv == 0 && H != 0)) return FA_ERR_INVALID_ARG;
+    if (empty || H == 0) return FA_OK;
+    if (H > 65535) return FA_ERR_UNSUPPORTED;
+    const long long R = (long long)(H / H_kv) * N_q;
+    const long long units = (long long)max_pages * page_size / kv4::kUnit + 2;   // most of one row block
+    if (R > 0x3fffffffLL || units * H_kv > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
+    if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return FA_ERR_MISALIGNED;
+    if (workspace_bytes < layout(B, H, H_kv, N_q, d, fa_internal::current_num_sms()).total) return FA_ERR_INVALID_ARG;
+    int dev = -1, sms = 0;
+    st = ready_device(&dev, &sms);
+    if (st == FA_OK) st = prepare_attend(dev);
+    if (st != FA_OK) return st;
+    const Layout L = layout(B, H, H_kv, N_q, d, sms);
+    const int rb = row_block(R);
+    kv4::AttendParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_codes = static_cast<const uint8_t*>(k_codes);
+    p.k_scales = static_cast<const uint16_t*>(k_scales);
+    p.v_codes = static_cast<const uint8_t*>(v_codes);
+    p.v_scales = static_cast<const uint16_t*>(v_scales);
+    p.key_lens = key_lens;
+    p.q_lens = q_lens;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.pg = paging(block_table, num_pages, page_size, max_pages);
+    p.H_kv = H_kv;
+    p.N_q = N_q;
+    p.R = (int)R;
+    p.row_blocks = (int)((R + rb - 1) / rb);
+    p.scale_log2 = scale_log2;
+    p.causal = causal ? 1 : 0;
+    p.window = window_left < 0 ? -1 : window_left;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.part_ml = reinterpret_cast<float*>(ws + L.ml);
+    p.words = reinterpret_cast<unsigned long long*>(ws + L.words);
+    const long long entries = (long long)B * p.row_blocks;
+    // the line of units of one launch stays within int
+    const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    for (long long e0 = 0; e0 < entries; e0 += chunk) {
+        p.e0 = e0;
+        p.E = (int)std::min(chunk, entries - e0);
+        p.ticket = next_ticket();
+        if (d == 64)
+            rb == 8 ? launch_attend<64, 1>(p, sms, s) : launch_attend<64, 2>(p, sms, s);
+        else
+            rb == 8 ? launch_attend<128, 1>(p, sms, s) : launch_attend<128, 2>(p, sms, s);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail("kernel launch (4-bit cache attention)", e);
+    }
+    return FA_OK;
+}
+
+}  // extern "C"

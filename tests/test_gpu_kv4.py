@@ -1,0 +1,538 @@
+"""GPU parity of the 4-bit paged key/value cache (fa_kv4_append, fa_kv4_read, fa_fwd_kv4)
+against the fp64 oracle: every code, scale and value exactly, the attention within bounds
+derived from its roundings.
+"""
+import numpy as np
+import pytest
+
+import oracle.kv4 as kv4
+from io_aware_exact_24_b200.inputs import bf16_bits_to_f32, f32_to_bf16_bits, normal_bf16
+
+from fa_testutil import run_fa, to_device_bf16, to_host_f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from io_aware_exact_24_b200.build import build
+    build()
+
+
+def ints(x, dtype=np.int32):
+    import torch
+    return None if x is None else torch.from_numpy(np.ascontiguousarray(np.asarray(x, dtype))).cuda()
+
+
+class Cache:
+    """A cache on the GPU whose unwritten rows hold the worst there is (codes of ones, scales NaN)."""
+
+    def __init__(self, num_pages, H_kv, page_size, d, max_pages, table):
+        import torch
+        self.num_pages, self.H_kv, self.page_size, self.d, self.max_pages = num_pages, H_kv, page_size, d, max_pages
+        self.table = None if table is None else np.asarray(table, np.int32)
+        self.d_table = ints(table)
+        shape = (num_pages, H_kv, page_size)
+        new = lambda last, fill, t: torch.full((*shape, last), fill, dtype=t, device="cuda")
+        self.k_codes, self.v_codes = new(d // 2, 255, torch.uint8), new(d // 2, 255, torch.uint8)
+        self.k_scales = new(d // 32, float("nan"), torch.bfloat16)
+        self.v_scales = self.k_scales.clone()
+
+    @property
+    def buffers(self):
+        return self.k_codes, self.k_scales, self.v_codes, self.v_scales
+
+    @property
+    def sizes(self):
+        return self.d, self.num_pages, self.page_size, self.max_pages
+
+    def append(self, k, v, key_lens, new_lens=None):
+        from io_aware_exact_24_b200 import fa_kv4_append
+        B, H_kv, N, _ = k.shape
+        fa_kv4_append(k, v, *self.buffers, self.d_table, ints(key_lens), ints(new_lens), B, H_kv, N, *self.sizes)
+
+    def read(self, key_lens, N, first=None, B=None):
+        import torch
+        from io_aware_exact_24_b200 import fa_kv4_read
+        B = len(key_lens)
+        k = torch.full((B, self.H_kv, N, self.d), 7.0, dtype=torch.bfloat16, device="cuda")
+        v = k.clone()
+        fa_kv4_read(*self.buffers, self.d_table, ints(key_lens), ints(first), k, v, B, self.H_kv, N, *self.sizes)
+        return k, v
+
+    def host(self):
+        """Codes [pages, H_kv, page_size, d] and scales (float64) of K and V."""
+        out = []
+        for c, s in ((self.k_codes, self.k_scales), (self.v_codes, self.v_scales)):
+            out.append((kv4.unpack(c.cpu().numpy()), s.float().cpu().numpy().astype(np.float64)))
+        return out
+
+    def positions(self, b, L):
+        """K and V values [H_kv, L, d] of positions 0..L-1 of sequence b, and which of them have a page."""
+        (kc, ks), (vc, vs) = self.host()
+        k, v = np.zeros((self.H_kv, L, self.d)), np.zeros((self.H_kv, L, self.d))
+        there = np.zeros(L, bool)
+        for j in range(L):
+            at = kv4.place(j, b, self.table, self.page_size, self.max_pages, self.num_pages)
+            if at is not None:
+                there[j] = True
+                k[:, j] = kv4.values(kc[at[0], :, at[1]], ks[at[0], :, at[1]])
+                v[:, j] = kv4.values(vc[at[0], :, at[1]], vs[at[0], :, at[1]])
+        return k, v, there
+
+
+def tokens(B, H_kv, N, d, seed, sigma=1.0):
+    bits = [normal_bf16((B, H_kv, N, d), seed, t, sigma) for t in (1, 2)]
+    return [to_device_bf16(b) for b in bits], [bf16_bits_to_f32(b).astype(np.float64) for b in bits]
+
+
+# ---------------------------------------------------------------- writing and reading back
+
+# B, H_kv, N_new, d, page_size, max_pages, key_lens, new_lens, shuffled table
+WRITES = [
+    (1, 1, 1, 64, 16, 1, [1], None, False),
+    (1, 1, 1, 128, 16, 3, [48], None, True),
+    (3, 2, 1, 128, 32, 4, [1, 33, 128], None, True),
+    (2, 3, 37, 64, 16, 5, [37, 80], None, True),              # runs over page ends
+    (3, 5, 50, 128, 48, 2, [50, 20, 96], [50, 20, 7], True),  # padded batch; page size no power of two
+    (2, 2, 9, 128, 16, 2, [4, 40], [9, 9], True),             # starts before 0; ends past the pages
+    (2, 1, 6, 64, 64, 1, [0, 64], [0, 3], False),             # nothing new for one; dense cache
+    (1, 2, 5, 128, 16, 2, [10], [9], True),                   # new_lens above N_new: clamped
+    (1, 1, 130, 64, 16, 16, [256], None, True),
+]
+
+
+@pytest.mark.parametrize("B,H_kv,N,d,page,maxp,key_lens,new_lens,shuffled", WRITES)
+def test_append_writes_the_tokens_and_nothing_else(B, H_kv, N, d, page, maxp, key_lens, new_lens, shuffled):
+    import torch
+    num_pages = B * maxp + 2
+    rng = np.random.default_rng(5)
+    table = rng.permutation(num_pages)[:B * maxp].reshape(B, maxp) if shuffled else None
+    c = Cache(num_pages, H_kv, page, d, maxp, table)
+    (k, v), host = tokens(B, H_kv, N, d, 11)
+    c.append(k, v, key_lens, new_lens)
+    torch.cuda.synchronize()
+    want = [(np.full((num_pages, H_kv, page, d), 15, np.uint8), np.full((num_pages, H_kv, page, d // 32), np.nan))
+            for _ in range(2)]
+    for x, (codes, scales) in zip(host, want):
+        qc, qs = kv4.quantise(x)
+        for b in range(B):
+            n_new = N if new_lens is None else min(N, new_lens[b])
+            for n in range(n_new):
+                at = kv4.place(key_lens[b] - n_new + n, b, table, page, maxp, num_pages)
+                if at is not None:
+                    codes[at[0], :, at[1]] = qc[b, :, n]
+                    scales[at[0], :, at[1]] = qs[b, :, n]
+    for (codes, scales), (wc, ws) in zip(c.host(), want):
+        assert np.array_equal(codes, wc)
+        assert np.array_equal(scales, ws, equal_nan=True)
+    # reading back: what the cache holds, and zeros outside the sequence
+    for first in (None, [-3] * B, [5] * B):
+        kb, vb = c.read(key_lens, page * maxp + 7, first)
+        kb, vb = to_host_f64(kb), to_host_f64(vb)
+        for b in range(B):
+            L = min(max(key_lens[b], 0), page * maxp)
+            wk, wv, there = c.positions(b, L)
+            f = 0 if first is None else first[b]
+            for got, w in ((kb, wk), (vb, wv)):
+                full = np.zeros((H_kv, page * maxp + 7, d))
+                for n in range(full.shape[1]):
+                    if 0 <= f + n < L and there[f + n]:
+                        full[:, n] = w[:, f + n]
+                assert np.array_equal(got[b], full, equal_nan=True)
+
+
+def test_append_of_every_kind_of_value():
+    """Groups of ties, equal pairs, tiny, huge and non-finite values get the oracle's codes and scales."""
+    import torch
+    d, N = 128, 4096
+    rng = np.random.default_rng(6)
+    x = np.empty((1, 1, N, d))
+    for n in range(N):
+        kind = n % 8
+        m = np.ldexp(rng.integers(128, 256, d).astype(float), rng.integers(-12, 4, d)) * rng.choice([-1, 1], d)
+        if kind == 1:
+            m = rng.integers(-16, 17, d) * 2.0 ** -5             # many exact ties and equal pairs
+        elif kind == 2:
+            m *= 2.0 ** -112                                     # around the lower end
+        elif kind == 3:
+            m *= 2.0 ** 110                                      # around the upper end
+        elif kind == 4:
+            m = np.zeros(d)
+            m[n % d] = -(2.0 ** (n % 20 - 10))
+        elif kind == 5:
+            m[n % d] = [np.nan, np.inf, -np.inf][n % 3]
+        elif kind == 6:
+            m = np.abs(m)
+        x[0, 0, n] = m
+    bits = f32_to_bf16_bits(np.nan_to_num(x, nan=0.0, posinf=1.0, neginf=1.0).astype(np.float32))
+    bits = np.where(np.isnan(x), 0x7FC1, np.where(np.isposinf(x), 0x7F80, np.where(np.isneginf(x), 0xFF80, bits))).astype(np.uint16)
+    host = bf16_bits_to_f32(bits).astype(np.float64)
+    t = to_device_bf16(bits)
+    c = Cache(1, 1, N, d, 1, None)
+    c.append(t, t.clone(), [N])
+    torch.cuda.synchronize()
+    wc, ws = kv4.quantise(host)
+    assert np.isnan(ws).sum() > 500 and (ws == 0).sum() > 100
+    for codes, scales in c.host():
+        assert np.array_equal(scales[0], ws[0], equal_nan=True)
+        assert np.array_equal(codes[0], wc[0])
+
+
+def test_bad_pages_are_skipped_and_read_as_zeros():
+    import torch
+    table = [[2, -1, 0], [7, 1, 1 << 30]]
+    c = Cache(3, 2, 16, 64, 3, table)
+    before = [b.clone() for b in c.buffers]
+    (k, v), _ = tokens(2, 2, 48, 64, 12)
+    c.append(k, v, [48, 48])
+    torch.cuda.synchronize()
+    # every page is written by exactly one of the named places
+    assert not any(torch.isnan(s.float()).any() for s in (c.k_scales, c.v_scales))
+    kb, vb = c.read([48, 48], 48)
+    torch.cuda.synchronize()
+    for got, x in ((kb, k), (vb, v)):
+        for b, bad in ((0, [1]), (1, [0, 2])):
+            for pg in range(3):
+                part = got[b, :, pg * 16:(pg + 1) * 16]
+                assert bool((part == 0).all()) == (pg in bad)
+    assert before[0].shape == c.k_codes.shape
+
+
+# ---------------------------------------------------------------- attention
+
+def bounds(q, k, v, seen, scale, o, lse):
+    """Largest |dO| [N, d] and |dLSE| [N] that the kernel's roundings allow, for one head.
+
+    Scores: exact products of 8-bit numbers summed in 32 bits, d/16 tensor-core steps and the
+    scale: (d/16 + 16 + 4) roundings of at most 2^-23 of the sum of magnitudes (truncating adds
+    counted), and two more of the score itself in the exponent.  2^x: 2^-22.  A weight is rounded
+    to bf16 and O divided by the sum of the rounded weights, so O moves by at most
+    (2^-8 (1 + 2^-7) + weight error) times the mean distance of V from O; sums of n weights in 32
+    bits by (n/16 + 40) 2^-23 of the mean magnitude; O rounds to bf16 once.  bf16 keeps 8
+    significant bits: numbers of [1, 2) are 2^-7 apart, so a rounding is off by up to 2^-8.
+    """
+    n, d = q.shape[0], q.shape[1]
+    eo, el = np.zeros((n, d)), np.zeros(n)
+    for i in range(n):
+        j = np.nonzero(seen[i])[0]
+        if j.size == 0:
+            continue
+        s = scale * (k[j] @ q[i])
+        mag = scale * (np.abs(k[j]) @ np.abs(q[i])).max()
+        p = np.exp(s - lse[i])
+        e_s = (d / 16 + 20) * 2.0 ** -23 * mag + 4 * 2.0 ** -23 * (np.abs(s).max() + abs(lse[i]) + 8) + 2.0 ** -21
+        e_n = (j.size / 16 + 40) * 2.0 ** -23
+        dist, size = p @ np.abs(v[j] - o[i]), p @ np.abs(v[j])
+        eo[i] = (2.0 ** -8 * (1 + 2.0 ** -7) + 2 * e_s) * dist + 2 * e_n * size
+        eo[i] += 2.0 ** -8 * (np.abs(o[i]) + eo[i])
+        el[i] = e_s + e_n + 2.0 ** -22 * (abs(lse[i]) + 8)
+    return eo, el
+
+
+def run_kv4(c, q, key_lens, q_lens, scale, causal, window, workspace=None, stream=None):
+    """fa_fwd_kv4 with guarded outputs; returns device tensors (o, lse) and whether the guards survived."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size
+    B, H, N, d = q.shape
+    guard = 256
+    o_buf = torch.full((q.numel() + 2 * guard,), -12345.0, dtype=torch.bfloat16, device="cuda")
+    l_buf = torch.full((B * H * N + 2 * guard,), -777.0, dtype=torch.float32, device="cuda")
+    o, lse = o_buf[guard:-guard].view(B, H, N, d), l_buf[guard:-guard].view(B, H, N)
+    n = fa_fwd_kv4_workspace_size(B, H, c.H_kv, N, d)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") if workspace is None else workspace
+    fa_fwd_kv4(q, *c.buffers, c.d_table, ints(key_lens), ints(q_lens), o, lse, B, H, c.H_kv, N, *c.sizes, scale, causal,
+               window, ws, n, stream)
+    torch.cuda.synchronize()
+    ok = bool((o_buf[:guard] == -12345.0).all() and (o_buf[-guard:] == -12345.0).all()
+              and (l_buf[:guard] == -777.0).all() and (l_buf[-guard:] == -777.0).all())
+    return o, lse, ok
+
+
+def check(c, q_bits, key_lens, q_lens, scale, causal, window, o, lse, heads=None, what=""):
+    """Compare with the oracle, element by element, within the derived bounds."""
+    q = bf16_bits_to_f32(q_bits).astype(np.float64)
+    B, H, N, d = q.shape
+    o, lse = to_host_f64(o), lse.cpu().numpy().astype(np.float64)
+    top = c.max_pages * c.page_size
+    worst = 0.0
+    for b in range(B):
+        L = min(max(int(key_lens[b]), 0), top)
+        ql = N if q_lens is None else min(max(int(q_lens[b]), 0), N)
+        k, v, there = c.positions(b, L)
+        seen = kv4.visible_keys(N, ql, L, L, causal, window) & there[None, :]
+        for h in (range(H) if heads is None else heads):
+            kh, vh = k[h // (H // c.H_kv)], v[h // (H // c.H_kv)]
+            ro, rl = kv4.attend(q[b, h], kh, vh, seen, scale)
+            eo, el = bounds(q[b, h], kh, vh, seen, scale, ro, rl)
+            empty = ~seen.any(1)
+            assert np.all(np.isneginf(lse[b, h][empty])) and np.all(o[b, h][empty] == 0), f"{what}: empty rows"
+            assert not np.signbit(o[b, h][empty]).any()
+            nan = np.isnan(ro)
+            assert np.array_equal(nan, np.isnan(o[b, h])), f"{what}: NaN"
+            assert np.array_equal(np.isnan(rl), np.isnan(lse[b, h])), f"{what}: NaN in the LSE"
+            fine = ~nan & ~empty[:, None]
+            ratio = (np.abs(o[b, h] - ro)[fine] / np.maximum(eo[fine], 1e-30)).max(initial=0.0)
+            live = ~empty & ~np.isnan(rl)
+            lr = (np.abs(lse[b, h][live] - rl[live]) / el[live]).max(initial=0.0)
+            assert ratio <= 1.0, f"{what}: b {b} h {h}: |dO| {ratio:.2f} of its bound"
+            assert lr <= 1.0, f"{what}: b {b} h {h}: |dLSE| {lr:.2f} of its bound"
+            worst = max(worst, ratio)
+    return worst
+
+
+def filled(B, H_kv, page, d, maxp, key_lens, seed, table="shuffled", sigma=1.0, edit=None):
+    """A cache filled through fa_kv4_append; unwritten rows stay NaN."""
+    num_pages = B * maxp + 1
+    rng = np.random.default_rng(seed)
+    t = rng.permutation(num_pages)[:B * maxp].reshape(B, maxp) if isinstance(table, str) else table
+    c = Cache(num_pages, H_kv, page, d, maxp, t)
+    L = max(1, max(min(max(n, 0), page * maxp) for n in key_lens))
+    bits = [normal_bf16((B, H_kv, L, d), seed, i, sigma) for i in (1, 2)]
+    if edit is not None:
+        edit(*bits)
+    k, v = (to_device_bf16(x) for x in bits)
+    c.append(k, v, [L] * B)
+    # what lies behind a sequence's length is made the worst there is again
+    import torch
+    worst = Cache(num_pages, H_kv, page, d, maxp, t)
+    for b, n in enumerate(key_lens):
+        for j in range(min(max(n, 0), page * maxp)):
+            at = kv4.place(j, b, c.table, page, maxp, num_pages)
+            if at is not None:
+                for w, x in zip(worst.buffers, c.buffers):
+                    w[at[0], :, at[1]] = x[at[0], :, at[1]]
+    torch.cuda.synchronize()
+    return worst
+
+
+# B, H, H_kv, N_q, d, page_size, max_pages, key_lens, q_lens, causal, window
+ATTEND = [
+    (1, 1, 1, 1, 64, 16, 1, [1], None, False, -1),
+    (1, 1, 1, 1, 128, 16, 1, [1], None, True, -1),
+    (1, 1, 1, 1, 128, 16, 2, [17], None, False, -1),
+    (2, 4, 2, 1, 128, 16, 20, [300, 0], None, False, -1),             # a sequence without keys
+    (3, 6, 6, 1, 64, 32, 12, [129, 383, 1], None, True, -1),
+    (1, 8, 1, 1, 128, 48, 20, [911], None, False, -1),                # 8 rows; pages of 48
+    (1, 9, 1, 1, 64, 16, 20, [303], None, False, -1),                 # 9 rows: a second block of one
+    (2, 24, 2, 1, 128, 64, 3, [100, 190], None, False, 50),
+    (2, 2, 1, 5, 128, 16, 16, [250, 6], None, True, -1),
+    (2, 4, 1, 5, 64, 16, 16, [250, 6], [5, 3], True, 20),             # ragged queries, window
+    (3, 2, 2, 7, 128, 16, 4, [3, 40, 64], [7, 0, 2], True, -1),       # more queries than keys; none
+    (1, 2, 1, 33, 128, 32, 8, [201], None, True, -1),
+    (1, 4, 2, 40, 64, 32, 8, [201], None, True, 64),
+    (2, 2, 1, 100, 128, 16, 8, [128, 100], [64, 100], True, -1),
+    (2, 3, 3, 20, 64, 16, 8, [128, 90], None, False, 30),
+    (1, 2, 2, 1, 128, 64, 40, [2500], None, False, 0),                # window 0: one key
+    (1, 1, 1, 1, 128, 256, 16, [4096], None, False, -1),              # one head over many CTAs
+    (1, 1, 1, 3, 64, 4096, 1, [4001], None, True, 3000),              # one page, window over many CTAs
+    (40, 2, 2, 1, 64, 16, 4, list(range(1, 41)), None, False, -1),    # many short sequences
+]
+
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,key_lens,q_lens,causal,window", ATTEND)
+def test_attention_matches_the_oracle(B, H, H_kv, N, d, page, maxp, key_lens, q_lens, causal, window):
+    c = filled(B, H_kv, page, d, maxp, key_lens, 21)
+    bits = normal_bf16((B, H, N, d), 22, 0)
+    scale = float(np.float32(d ** -0.5))
+    o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, q_lens, scale, causal, window)
+    assert guards
+    check(c, bits, key_lens, q_lens, scale, causal, window, o, lse)
+
+
+@pytest.mark.parametrize("sigma,scale", [(4.0, 0.5), (0.05, 1.0), (1.0, 30.0), (2.0 ** -60, 1.0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_on_steep_and_flat_scores(sigma, scale, d):
+    # steep: scores up to thousands, one key takes all; flat: every key counts alike
+    key_lens = [700, 333]
+    c = filled(2, 1, 16, d, 44, key_lens, 31, sigma=sigma)
+    bits = normal_bf16((2, 3, 2, d), 32, 0, min(sigma, 4.0))
+    o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, None, scale, True, -1)
+    assert guards
+    check(c, bits, key_lens, None, scale, True, -1, o, lse, what=f"sigma {sigma}")
+
+
+def test_scores_that_grow_along_the_keys():
+    # every tile moves the reference max: all the rescaling there is
+    def edit(k, v):
+        ramp = np.linspace(0.0, 6.0, k.shape[2])[None, None, :, None]
+        k[:] = f32_to_bf16_bits((0.01 * bf16_bits_to_f32(k) + ramp).astype(np.float32))
+    c = filled(1, 2, 16, 128, 60, [960], 33, edit=edit)
+    bits = f32_to_bf16_bits(np.ones((1, 4, 1, 128), np.float32))
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [960], None, 0.5, False, -1)
+    check(c, bits, [960], None, 0.5, False, -1, o, lse)
+
+
+@pytest.mark.parametrize("N,rows", [(3, 3), (12, 24)])
+def test_what_a_query_does_not_see_has_no_influence(N, rows):
+    # keys and values of the last tokens are NaN or infinite: the queries before them stay clean,
+    # those that see them do not
+    def edit(k, v):
+        k[0, :, -2, 5] = 0x7FC0
+        v[0, :, -1, 70] = 0x7F80
+    key_lens = [200]
+    c = filled(1, 1, 16, 128, 13, key_lens, 34, edit=edit)
+    bits = normal_bf16((1, rows // N, N, 128), 35, 0)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, -1)
+    check(c, bits, key_lens, None, 0.09, True, -1, o, lse)
+    import torch
+    assert not torch.isnan(o[:, :, :N - 2].float()).any() and torch.isnan(o[:, :, N - 2:].float()).all()
+    # behind a window too: an early poisoned value is out of sight of the last query
+    def edit2(k, v):
+        v[0, :, 190, 3] = 0xFF80
+    c = filled(1, 1, 16, 128, 13, key_lens, 34, edit=edit2)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, 8)
+    check(c, bits, key_lens, None, 0.09, True, 8, o, lse)
+
+
+def test_bad_pages_are_masked():
+    table = [[0, -1, 5, 2, 99, 1]]
+    c = filled(1, 2, 16, 64, 6, [90], 36, table=table)
+    bits = normal_bf16((1, 4, 3, 64), 37, 0)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [90], None, 0.125, True, -1)
+    check(c, bits, [90], None, 0.125, True, -1, o, lse)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [5000], [2], 0.125, True, -1)     # length clamped to the pages
+    check(c, bits, [5000], [2], 0.125, True, -1, o, lse)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [-3], None, 0.125, False, -1)
+    check(c, bits, [-3], None, 0.125, False, -1, o, lse)
+
+
+def test_more_sequences_than_one_launch_takes():
+    import torch
+    B = 1500
+    key_lens = [(7 * b) % 40 for b in range(B)]
+    c = Cache(B, 1, 48, 64, 1, None)
+    (k, v), _ = tokens(B, 1, 48, 64, 41)
+    c.append(k, v, [48] * B)
+    bits = normal_bf16((B, 2, 1, 64), 42, 0)
+    o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.125, False, -1)
+    assert guards
+    check(c, bits, key_lens, None, 0.125, False, -1, o, lse)
+    torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    import torch
+    H_kv, page, d = 8, 1024, 128
+    num_pages = (1 << 32) // (H_kv * page * d // 2) + 8      # codes of K alone exceed 2^32 bytes
+    shape = (num_pages, H_kv, page)
+    c = Cache(1, H_kv, page, d, 2, None)
+    c.num_pages = num_pages
+    c.k_codes = torch.empty((*shape, d // 2), dtype=torch.uint8, device="cuda")
+    c.v_codes = torch.empty_like(c.k_codes)
+    c.k_scales = torch.empty((*shape, d // 32), dtype=torch.bfloat16, device="cuda")
+    c.v_scales = torch.empty_like(c.k_scales)
+    c.table = np.array([[num_pages - 1, num_pages - 3]], np.int32)
+    c.d_table = ints(c.table)
+    (k, v), host = tokens(1, H_kv, 1100, d, 43)
+    c.append(k, v, [1100])
+    kb, vb = c.read([1100], 1100)
+    torch.cuda.synchronize()
+    for got, x in ((kb, host[0]), (vb, host[1])):
+        assert np.array_equal(to_host_f64(got), kv4.values(*kv4.quantise(x)))
+    bits = normal_bf16((1, 2 * H_kv, 1, d), 44, 0)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [1100], None, 0.088, False, -1)
+    ks, vs = to_host_f64(kb), to_host_f64(vb)
+    q = bf16_bits_to_f32(bits).astype(np.float64)
+    seen = np.ones((1, 1100), bool)
+    for h in (0, 7, 15):
+        ro, rl = kv4.attend(q[0, h], ks[0, h // 2], vs[0, h // 2], seen, 0.088)
+        eo, el = bounds(q[0, h], ks[0, h // 2], vs[0, h // 2], seen, 0.088, ro, rl)
+        assert np.all(np.abs(to_host_f64(o)[0, h] - ro) <= eo)
+        assert np.all(np.abs(lse.cpu().numpy()[0, h] - rl) <= el)
+
+
+def test_results_are_the_same_bits_each_time_and_on_another_stream():
+    import torch
+    key_lens = [1900, 5, 777]
+    c = filled(3, 2, 16, 128, 120, key_lens, 51)
+    q = to_device_bf16(normal_bf16((3, 8, 2, 128), 52, 0))
+    o, lse, _ = run_kv4(c, q, key_lens, None, 0.09, True, -1)
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        o2, lse2, _ = run_kv4(c, q, key_lens, None, 0.09, True, -1, stream=stream)
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+def test_a_decoding_loop_matches_the_dense_forward():
+    """Append, read back and attend as a serving loop does: a prompt, then tokens one by one."""
+    import torch
+    B, H, H_kv, d, page, maxp = 2, 4, 2, 128, 16, 8
+    prompt, steps = [70, 33], 4
+    rng = np.random.default_rng(61)
+    c = Cache(B * maxp, H_kv, page, d, maxp, rng.permutation(B * maxp).reshape(B, maxp))
+    (k, v), _ = tokens(B, H_kv, max(prompt), d, 62)
+    c.append(k, v, prompt, prompt)
+    lens = list(prompt)
+    for s in range(steps):
+        (k1, v1), _ = tokens(B, H_kv, 1, d, 63 + s)
+        lens = [n + 1 for n in lens]
+        c.append(k1, v1, lens)
+        bits = normal_bf16((B, H, 1, d), 80 + s, 0)
+        o, lse, guards = run_kv4(c, to_device_bf16(bits), lens, None, 0.088, True, -1)
+        assert guards
+        check(c, bits, lens, None, 0.088, True, -1, o, lse, what=f"step {s}")
+        # the dense forward on what is read back sees the same numbers (each within its own rounding)
+        kb, vb = c.read(lens, max(lens))
+        kd, vd = (x.repeat_interleave(H // H_kv, 1).contiguous().view(torch.int16).cpu().numpy().view(np.uint16) for x in (kb, vb))
+        od, ld = run_fa(bits, kd, vd, 0.088, False, lens)
+        assert np.abs(od - to_host_f64(o)).max() <= 2.0 ** -7 * np.abs(to_host_f64(vb)).max()
+        assert np.abs(ld - lse.cpu().numpy()).max() <= 1e-4
+
+
+def test_captured_calls_replay_and_graphs_share_a_workspace():
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
+    B, H, H_kv, d, page, maxp = 2, 4, 1, 64, 16, 100
+    c = Cache(B * maxp, H_kv, page, d, maxp, None)
+    (k, v), _ = tokens(B, H_kv, 1500, d, 71)
+    c.append(k, v, [1500, 1500])
+    lens = ints([900, 1400])
+    (k1, v1), _ = tokens(B, H_kv, 1, d, 72)
+    n = max(fa_fwd_kv4_workspace_size(B, H, H_kv, N, d) for N in (1, 5))
+    ws = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for N in (1, 5):
+        bits = normal_bf16((B, H, N, d), 73, 0)
+        q = to_device_bf16(bits)
+        o, lse = torch.empty_like(q), torch.empty((B, H, N), dtype=torch.float32, device="cuda")
+        kb = torch.empty((B, H_kv, 3, d), dtype=torch.bfloat16, device="cuda")
+        vb = torch.empty_like(kb)
+
+        def step():
+            fa_kv4_append(k1, v1, *c.buffers, None, lens, None, B, H_kv, 1, *c.sizes)
+            fa_kv4_read(*c.buffers, None, lens, None, kb, vb, B, H_kv, 3, *c.sizes)
+            fa_fwd_kv4(q, *c.buffers, None, lens, None, o, lse, B, H, H_kv, N, *c.sizes, 0.125, True, -1, ws, n)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        graphs.append((graph, bits, o, lse, (q, kb, vb)))     # a graph's buffers live as long as it does
+    for new in ([900, 1400], [17, 1500], [1500, 1], [1500, 1], [640, 641]):
+        lens.copy_(ints(new))
+        for graph, *_ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, bits, o, lse, _ in graphs:
+            check(c, bits, new, None, 0.125, True, -1, o, lse, what=str(new))
+
+
+def test_workspace_contents_do_not_matter_and_nothing_past_it_is_touched():
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4_workspace_size
+    key_lens = [3000]
+    c = filled(1, 1, 64, 128, 50, key_lens, 91)
+    q = to_device_bf16(normal_bf16((1, 2, 8, 128), 92, 0))
+    n = fa_fwd_kv4_workspace_size(1, 2, 1, 8, 128)
+    want = None
+    for fill in (0, 0xFF, 0x7F):
+        buf = torch.full((n + 512,), fill, dtype=torch.uint8, device="cuda")
+        o, lse, _ = run_kv4(c, q, key_lens, None, 0.09, True, -1, workspace=buf)
+        assert bool((buf[n:] == fill).all())
+        if want is not None:
+            assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+        want = (o, lse)

@@ -1,0 +1,185 @@
+"""CPU tests of the 4-bit key/value cache: the format's oracle against hand-worked groups and
+its own properties, and the refusals of the entry points (no GPU touched)."""
+import numpy as np
+import pytest
+
+import oracle.kv4 as kv4
+from io_aware_exact_24_b200 import binding
+from io_aware_exact_24_b200.build import build
+from io_aware_exact_24_b200.inputs import bf16_bits_to_f32, f32_to_bf16_bits, normal_bf16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return binding.load_library()
+
+
+# ---------------------------------------------------------------- the format
+
+def test_a_hand_worked_group():
+    # m = -4: s = 0.5 (16 * 2^-5); codes are x / 0.5 + 8, 3.6 -> 7.2 -> 15 and +4 -> 8 clamps to 15
+    x = np.zeros(32)
+    x[:6] = [-4.0, 4.0 - 2 ** -6, 3.6, 0.25, 0.75, -0.26]
+    codes, s = kv4.quantise(x)
+    assert s[0] == 0.5
+    # 0.25 / 0.5 and 0.75 / 0.5 are ties: to the even 0 and 2
+    assert list(codes[:7]) == [0, 15, 15, 8, 10, 7, 8]
+    assert list(kv4.values(codes, s)[:6]) == [-4.0, 3.5, 3.5, 0.0, 1.0, -0.5]
+
+
+def test_the_sign_of_the_scale_follows_the_extreme_value():
+    x = np.zeros(32)
+    x[3], x[9] = 6.0, -6.0
+    codes, s = kv4.quantise(x)                  # an equal pair: the positive one sets the sign
+    assert s[0] == -0.75 and codes[3] == 0 and codes[9] == 15
+    codes, s = kv4.quantise(-np.abs(x))
+    assert s[0] == 0.75 and codes[3] == 0 and codes[9] == 0
+
+
+@pytest.mark.parametrize("m,s", [(1.0, -0.125), (255 / 128, -0.25), (131 / 128, -0.125 * 16 / 16),
+                                 (133 / 128, -0.125 * 17 / 16), (132 / 128, -0.125 * 16 / 16),
+                                 (140 / 128, -0.125 * 18 / 16), (-140 / 128, 0.125 * 18 / 16)])
+def test_scales_round_to_five_bits_ties_to_even(m, s):
+    # |m| * 128 = 131 .. 133 stand 3/8, 4/8 (a tie: down to the even 16) and 5/8 between 16 and 17;
+    # 140 is the tie between 17 and 18; 255 rounds up into the next power of two
+    x = np.zeros(32)
+    x[5] = m
+    assert kv4.scale_of(x) == s
+
+
+def test_values_are_bf16_numbers_and_near():
+    x = bf16_bits_to_f32(normal_bf16((64, 128), 3, 0)).astype(np.float64)
+    codes, s = kv4.quantise(x)
+    y = kv4.values(codes, s)
+    assert np.array_equal(bf16_bits_to_f32(f32_to_bf16_bits(y.astype(np.float32))).astype(np.float64), y)
+    step = np.abs(np.repeat(s, 32, axis=-1))
+    # half a step, or up to 1.25 steps next to the value opposite to the extreme one
+    assert np.all(np.abs(x - y) <= np.where(np.abs(x) > 7.5 * step, 1.25, 0.5) * step)
+    assert np.array_equal(kv4.unpack(kv4.pack(codes)), codes)
+
+
+@pytest.mark.parametrize("bad,want", [(np.nan, "nan"), (np.inf, "nan"), (-np.inf, "nan"), (2.0 ** 121, "nan"),
+                                      (2.0 ** -108, "zero"), (2.0 ** 120, "value"), (2.0 ** -107, "value")])
+def test_ends_of_the_range(bad, want):
+    x = np.zeros((1, 64))
+    x[0, 7] = bad
+    y = kv4.values(*kv4.quantise(x))
+    assert np.all(y[0, 32:] == 0)               # the other group does not notice
+    if want == "nan":
+        assert np.all(np.isnan(y[0, :32]))
+    elif want == "zero":
+        assert np.all(y[0, :32] == 0)
+    else:
+        assert y[0, 7] == bad
+
+
+def test_attend_ignores_what_a_query_does_not_see():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.normal(size=(3, 64)), rng.normal(size=(9, 64)), rng.normal(size=(9, 64))
+    seen = kv4.visible_keys(3, 3, 7, 9, True, 2)
+    assert seen.tolist() == [[j in r for j in range(9)] for r in ((2, 3, 4), (3, 4, 5), (4, 5, 6))]
+    o, lse = kv4.attend(q, k, v, seen, 0.125)
+    k[[0, 1, 7, 8]] = np.nan
+    v[[0, 1, 7, 8]] = np.inf
+    o2, lse2 = kv4.attend(q, k, v, seen, 0.125)
+    assert np.array_equal(o, o2) and np.array_equal(lse, lse2)
+    for i, r in enumerate(((2, 3, 4), (3, 4, 5), (4, 5, 6))):
+        p = np.exp(0.125 * k[list(r)] @ q[i])
+        np.testing.assert_allclose(o[i], p @ v[list(r)] / p.sum(), rtol=1e-12)
+        np.testing.assert_allclose(lse[i], np.log(p.sum()), rtol=1e-12)
+    assert kv4.visible_keys(4, 2, 7, 7, False, -1).sum(1).tolist() == [7, 7, 0, 0]
+    assert kv4.visible_keys(5, 5, 2, 4, True, -1).sum(1).tolist() == [0, 0, 0, 1, 2]
+
+
+def test_places():
+    assert kv4.place(-1, 0, None, 16, 2, 9) is None and kv4.place(32, 0, None, 16, 2, 9) is None
+    assert kv4.place(17, 3, None, 16, 2, 9) == (7, 1) and kv4.place(17, 4, None, 16, 2, 9) is None
+    assert kv4.place(17, 0, [[4, 9]], 16, 2, 9) is None and kv4.place(15, 0, [[4, 9]], 16, 2, 9) == (4, 15)
+    assert kv4.place(15, 0, [[-1, 9]], 16, 2, 9) is None
+
+
+# ---------------------------------------------------------------- refusals
+
+P = 1 << 20   # a fake, suitably aligned address: validation must fail before it is used
+INVALID, UNSUPPORTED, MISALIGNED = binding.FA_ERR_INVALID_ARG, binding.FA_ERR_UNSUPPORTED, binding.FA_ERR_MISALIGNED
+
+
+def append(k=P, v=P, kc=P, ks=P, vc=P, vs=P, table=P, key_lens=P, lens=P, B=1, H_kv=1, N=1, d=64, num_pages=4,
+           page_size=16, max_pages=4):
+    return binding.fa_kv4_append(k, v, kc, ks, vc, vs, table, key_lens, lens, B, H_kv, N, d, num_pages, page_size,
+                                 max_pages, stream=0, check=False)
+
+
+def read(k=P, v=P, kc=P, ks=P, vc=P, vs=P, table=P, key_lens=P, lens=P, B=1, H_kv=1, N=1, d=64, num_pages=4,
+         page_size=16, max_pages=4):
+    return binding.fa_kv4_read(kc, ks, vc, vs, table, key_lens, lens, k, v, B, H_kv, N, d, num_pages, page_size,
+                               max_pages, stream=0, check=False)
+
+
+def fwd(q=P, o=P, lse=P, kc=P, ks=P, vc=P, vs=P, table=P, key_lens=P, lens=P, B=1, H=2, H_kv=1, N=1, d=64,
+        num_pages=4, page_size=16, max_pages=4, scale=0.125, causal=0, window=-1, ws=P, ws_bytes=1 << 40):
+    return binding.fa_fwd_kv4(q, kc, ks, vc, vs, table, key_lens, lens, o, lse, B, H, H_kv, N, d, num_pages, page_size,
+                              max_pages, scale, causal, window, ws, ws_bytes, stream=0, check=False)
+
+
+SHARED = [
+    (dict(d=32), UNSUPPORTED), (dict(d=256), UNSUPPORTED),
+    (dict(B=-1), INVALID), (dict(H_kv=-1), INVALID), (dict(N=-1), INVALID), (dict(num_pages=-1), INVALID),
+    (dict(max_pages=-1), INVALID), (dict(page_size=0), INVALID), (dict(page_size=-16), INVALID),
+    (dict(page_size=24), INVALID), (dict(page_size=8), INVALID),
+    (dict(page_size=1 << 20, max_pages=(1 << 10) + 1), UNSUPPORTED),
+    (dict(B=70000), UNSUPPORTED),
+    (dict(key_lens=None), INVALID), (dict(kc=None), INVALID), (dict(ks=None), INVALID), (dict(vc=None), INVALID),
+    (dict(vs=None), INVALID),
+    (dict(kc=P + 8), MISALIGNED), (dict(ks=P + 2), MISALIGNED), (dict(vc=P + 4), MISALIGNED), (dict(vs=P + 8), MISALIGNED),
+    (dict(table=P + 2), MISALIGNED), (dict(key_lens=P + 1), MISALIGNED), (dict(lens=P + 3), MISALIGNED),
+]
+TOKENS = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=P + 8), MISALIGNED), (dict(v=P + 2), MISALIGNED),
+          (dict(H_kv=65536), UNSUPPORTED), (dict(B=65535, H_kv=65535, N=1 << 10), UNSUPPORTED)]
+FWD = [
+    (dict(H=3, H_kv=2), INVALID), (dict(H=-2), INVALID), (dict(H=65536), UNSUPPORTED),
+    (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=1e-46), INVALID),
+    (dict(q=None), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(ws=None), INVALID),
+    (dict(q=P + 8), MISALIGNED), (dict(o=P + 4), MISALIGNED), (dict(lse=P + 2), MISALIGNED), (dict(ws=P + 128), MISALIGNED),
+    (dict(ws_bytes=1024), INVALID), (dict(N=1 << 30, H=8), UNSUPPORTED),
+    (dict(H=4096, H_kv=4096, page_size=1 << 20, max_pages=1 << 10), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("call,kw,code",
+                         [(c, kw, code) for c in (append, read) for kw, code in SHARED + TOKENS]
+                         + [(fwd, kw, code) for kw, code in SHARED + FWD],
+                         ids=lambda x: x.__name__ if callable(x) else str(x))
+def test_refusals_come_before_any_cuda_call(lib, call, kw, code):
+    assert call(**kw) == code
+
+
+@pytest.mark.parametrize("call", [append, read, fwd])
+@pytest.mark.parametrize("kw", [dict(B=0), dict(N=0), dict(B=0, kc=None, key_lens=None, table=None)], ids=str)
+def test_empty_problems_are_noops(lib, call, kw):
+    assert call(**kw) == binding.FA_OK
+
+
+def test_no_heads_is_a_noop(lib):
+    assert append(H_kv=0) == read(H_kv=0) == fwd(H=0) == fwd(H=0, H_kv=0) == binding.FA_OK
+    assert fwd(H=2, H_kv=0) == INVALID
+
+
+def test_without_a_gpu_valid_calls_report_no_device(lib):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("would launch on fake addresses")
+    for call in (append, read, fwd):
+        assert call() == binding.FA_ERR_NO_DEVICE
+        assert call(table=None, lens=None) == binding.FA_ERR_NO_DEVICE
+        assert call(num_pages=0, kc=None, ks=None, vc=None, vs=None) == binding.FA_ERR_NO_DEVICE
+
+
+def test_workspace_size(lib):
+    n = binding.fa_fwd_kv4_workspace_size(3, 8, 2, 1, 128)
+    assert n > 0 and n % 256 == 0
+    assert binding.fa_fwd_kv4_workspace_size(3, 8, 2, 5, 128) > 0
+    for bad in ((0, 8, 2, 1, 128), (3, 8, 3, 1, 128), (3, 8, 0, 1, 128), (3, 8, 2, 0, 128), (3, 8, 2, 1, 96), (3, -8, 2, 1, 64)):
+        assert binding.fa_fwd_kv4_workspace_size(*bad) == 0
