@@ -33,6 +33,8 @@ int validate(const void* k_codes, const void* k_scales, const void* v_codes, con
     if (page_size % 16 != 0) return FA_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     if ((long long)max_pages * page_size > kMaxPositions) return FA_ERR_UNSUPPORTED;
+    // rows of one head's tokens are numbered in 32 bits (a cache of 2^32 rows is over 300 GB)
+    if ((unsigned __int128)num_pages * H_kv * page_size >= ((unsigned __int128)1 << 32)) return FA_ERR_UNSUPPORTED;
     *empty = B == 0 || H_kv == 0 || N == 0;
     if (*empty) return FA_OK;
     if (B > 65535 || H_kv > 65535) return FA_ERR_UNSUPPORTED;
@@ -75,7 +77,7 @@ unsigned long long next_ticket() {
 
 // Rows per block: one MMA column block holds 8 query rows.
 int row_block(long long R) { return R <= 8 ? 8 : 16; }
-int ctas_per_sm(int rb) { return rb == 8 ? 2 : 1; }
+int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
 
 // Workspace of the attention: two partial results per CTA, then the arrival words.
 struct Layout {
@@ -220,12 +222,13 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     if (R > 0x3fffffffLL || units * H_kv > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
     if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return FA_ERR_MISALIGNED;
-    if (workspace_bytes < layout(B, H, H_kv, N_q, d, fa_internal::current_num_sms()).total) return FA_ERR_INVALID_ARG;
     int dev = -1, sms = 0;
     st = ready_device(&dev, &sms);
+    if (st != FA_OK) sms = fa_internal::current_num_sms();
+    const Layout L = layout(B, H, H_kv, N_q, d, sms);
+    if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
     if (st == FA_OK) st = prepare_attend(dev);
     if (st != FA_OK) return st;
-    const Layout L = layout(B, H, H_kv, N_q, d, sms);
     const int rb = row_block(R);
     kv4::AttendParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -254,7 +257,8 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     for (long long e0 = 0; e0 < entries; e0 += chunk) {
-        p.e0 = e0;
+        p.b0 = (int)(e0 / p.row_blocks);
+        p.rb0 = (int)(e0 % p.row_blocks);
         p.E = (int)std::min(chunk, entries - e0);
         p.ticket = next_ticket();
         if (d == 64)
