@@ -43,6 +43,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load the compiled library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -122,19 +124,31 @@ def _addr(x) -> int | None:
     """Raw address of a torch tensor / numpy array / int / None."""
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
     if hasattr(x, "ctypes"):
         return int(x.ctypes.data)
     raise TypeError(f"cannot take the address of {type(x)!r}")
 
 
+_raw_stream = None   # (device of this thread, its current stream), where torch offers them as plain numbers
+
+
 def _stream(stream) -> int | None:
+    global _raw_stream
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            import torch
+            handle = int(torch.cuda.current_stream().cuda_stream)   # initialises CUDA if need be
+            get = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _raw_stream = get if all(get) else (lambda: None, lambda _: int(torch.cuda.current_stream().cuda_stream))
+            return handle
+        device, current = _raw_stream
+        return current(device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

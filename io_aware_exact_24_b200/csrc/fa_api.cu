@@ -584,13 +584,14 @@ namespace fa_internal {
 int cuda_fail(const char* what, cudaError_t e) { return ::cuda_fail(what, e); }
 
 int ready_device(int* dev, int* num_sms) {
-    int ndev = 0;
-    if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev == 0) {
-        cudaGetLastError();
-        return FA_ERR_NO_DEVICE;
-    }
     const cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return ::cuda_fail("cudaGetDevice", e);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        int n = 0;
+        const bool none = cudaGetDeviceCount(&n) != cudaSuccess || n == 0;
+        cudaGetLastError();
+        return none ? FA_ERR_NO_DEVICE : ::cuda_fail("cudaGetDevice", e);
+    }
     const int st = prepare_device(*dev);
     if (st == FA_OK) *num_sms = g_dev[*dev].num_sms;
     return st;

@@ -55,7 +55,7 @@ kv4::Paging paging(const int32_t* table, int num_pages, int page_size, int max_p
     pg.num_pages = num_pages;
     pg.page_size = page_size;
     pg.max_pages = max_pages;
-    pg.magic = 0xffffffffu / (uint32_t)page_size;
+    kv4::divisor((uint32_t)page_size, pg.magic, pg.shift);
     return pg;
 }
 
@@ -101,8 +101,11 @@ int g_status[64];
 
 template <int D, int NB>
 cudaError_t set_smem() {
-    return cudaFuncSetAttribute(kv4::attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kv4::Cfg<D, NB>::kSmemBytes);
+    const int bytes = kv4::Cfg<D, NB>::kSmemBytes;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv4::attend_kernel<D, NB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kv4::attend_kernel<D, NB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 int prepare_attend(int dev) {
     std::call_once(g_once[dev], [&] {
@@ -118,7 +121,10 @@ int prepare_attend(int dev) {
 template <int D, int NB>
 void launch_attend(const kv4::AttendParams& p, int num_sms, cudaStream_t s) {
     const int grid = num_sms * ctas_per_sm(8 * NB);
-    kv4::attend_kernel<D, NB><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
+    if (p.pg.page_size % kv4::kTile == 0)
+        kv4::attend_kernel<D, NB, true><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
+    else
+        kv4::attend_kernel<D, NB, false><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
 }
 
 }  // namespace

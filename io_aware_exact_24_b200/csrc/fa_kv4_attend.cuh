@@ -19,6 +19,8 @@
 // is merged by the last of them to finish, from partial results in the workspace.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_kv4_kernel.cuh"
 
 namespace fa {
@@ -57,7 +59,7 @@ struct AttendParams {
 template <int D, int NB>
 struct Cfg {
     static constexpr int kRB = 8 * NB;                        // rows per block
-    static constexpr int kCtasPerSm = NB == 1 ? 4 : 2;
+    static constexpr int kCtasPerSm = NB == 1 ? 3 : 2;
     static constexpr int kRow = D / 2;                        // bytes of codes per token
     static constexpr int kSRow = D / kGroup * 2;              // bytes of scales per token
     static constexpr int kStageBytes = 2 * kTile * (kRow + kSRow);
@@ -72,9 +74,8 @@ struct Cfg {
     static constexpr int kStatOff = kRedOff + kRedBytes;      // [kWarps][kRB] max, rounded sum, sum
     static constexpr int kStatBytes = 3 * kWarps * kRB * 4;
     static constexpr int kLimOff = kStatOff + kStatBytes;     // [kRB] first and one past the last visible key
-    static constexpr int kQOff = kLimOff + 2 * kRB * 4;       // NB > 1: [NB][D/16][32] B fragments
-    static constexpr int kQBytes = NB > 1 ? NB * (D / 16) * 32 * 8 : 0;
-    static constexpr int kPreOff = kQOff + kQBytes;           // [E + 1] first unit of an entry
+    static constexpr int kQOff = kRedOff;                     // [NB][D/32][32] pairs of B fragments; in turn with the exchange
+    static constexpr int kPreOff = kLimOff + 2 * kRB * 4;     // [E + 1] first unit of an entry
     static constexpr int kMiscOff = kPreOff + (kMaxEntries + 1) * 4;
     static constexpr int kSmemBytes = kMiscOff + 64;
     static_assert((kSmemBytes + 1024) * kCtasPerSm <= 233472, "shared memory of an SM");
@@ -117,16 +118,18 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
     return v;
 }
 
-// Arrivals of a call's CTAs at an item.  The word holds (ticket << 16) | count.  Before its
-// arrival a CTA makes sure that the word carries this call's ticket: one that finds
-// another (an earlier call, or what the workspace held) tries once to claim the word, and
-// whoever fails found it claimed.  The last arrival clears it, so that a captured call,
-// whose ticket is the same at each replay, starts anew.
-__device__ __forceinline__ void arrive_claim(unsigned long long* word, unsigned long long ticket) {
-    const unsigned long long cur = atomicAdd(word, 0ull);
-    if ((cur >> 16) != ticket) atomicCAS(word, cur, ticket << 16);
+// Arrivals of a call's CTAs at an item.  The word holds (ticket << 16) | count, and 0 after
+// a call.  At its segment's start a CTA tries to claim a 0 for this call's ticket; one that
+// found something else there (not a call's word: what the workspace held at first) tries
+// again from that value before it arrives, and whoever fails found the word claimed.  The
+// last arrival clears it, so that a captured call, whose ticket is the same at each replay,
+// starts anew.
+__device__ __forceinline__ unsigned long long arrive_claim(unsigned long long* word, unsigned long long ticket) {
+    return atomicCAS(word, 0ull, ticket << 16);
 }
-__device__ __forceinline__ bool arrive_last(unsigned long long* word, int n) {
+__device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long found, unsigned long long ticket,
+                                            int n) {
+    if (found != 0 && (found >> 16) != ticket) atomicCAS(word, found, ticket << 16);
     const unsigned long long old = atomicAdd(word, 1ull);
     if ((int)(old & 0xffffull) + 1 != n) return false;
     atomicExch(word, 0ull);
@@ -191,7 +194,7 @@ __device__ __forceinline__ Entry entry_of(const AttendParams& p, int e) {
     return x;
 }
 
-template <int D, int NB>
+template <int D, int NB, bool kOneRun>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kernel(const AttendParams p) {
     using C = Cfg<D, NB>;
     constexpr int RB = C::kRB;
@@ -275,16 +278,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         l_pos = l_lo + seg_k * kUnit;
     }
     int seg_e = l_e;
-    int l_page[2], l_off[2];
-    // pages of the cursor's tile, a step before the copies need them; a tile is two runs of
-    // 16 keys, each inside one page
-    auto look_up = [&](bool any) {
+    // A tile is kRuns runs of consecutive rows of the cache: one where page_size is a multiple
+    // of 32, else two of 16 keys.  Each lane looks up the page of one of the warp's next 32
+    // tiles of the item, a step before the first of them is copied.  A run that is not there
+    // (past the last visible key, or no page) is not copied, and masked.
+    constexpr int kRuns = kOneRun ? 1 : 2;
+    const int32_t* l_table = p.pg.table == nullptr ? nullptr : p.pg.table + (long long)l_b * p.pg.max_pages;
+    int l_page[kRuns], l_off[kRuns];             // of the lane's tile; page -1: not there
+    uint32_t l_row[kRuns];                       // and its first row in the cache
+    int l_at = 0, l_u = u0;                      // the next tile's lane, and the unit of lane 0
+    auto look_up = [&]() {
+        l_u += l_at;
+        l_at = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kRuns; ++i) {
+            const int pos = l_pos + lane * kUnit + 16 * i;
             l_page[i] = -1;
-            l_off[i] = 0;
-            const int pos = l_pos + 16 * i;
-            if (any && pos < l_hi) l_page[i] = page_of(p.pg, l_b, page_div(p.pg, pos, l_off[i]));
+            if (pos < l_hi && l_u + lane < u1) {
+                const int n = page_div(p.pg, pos, l_off[i]);
+                l_page[i] = l_table != nullptr ? __ldg(l_table + n) : l_b * p.pg.max_pages + n;
+            }
         }
     };
     const uint32_t ring = base + (uint32_t)(warp * C::kStages * C::kStageBytes);
@@ -304,39 +317,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         constexpr int kSC = kTile * C::kSRow / 16;               // chunks of a tile's scales, per tensor: 16 or 8
         const int c = lane % kSC;
         dst_s = (lane < kSC ? C::kKSOff : C::kVSOff) + c * 16;
-        src_s = reinterpret_cast<const uint8_t*>(lane < kSC ? p.k_scales : p.v_scales) + c % (kSC / 2) * 16;
+        src_s = reinterpret_cast<const uint8_t*>(lane < kSC ? p.k_scales : p.v_scales) + (kOneRun ? c : c % (kSC / 2)) * 16;
     }
-    const bool s_second = lane % (kTile * C::kSRow / 16) >= kTile * C::kSRow / 32;   // its scales are of the second run
-    uint32_t loaded = 0;             // two bits per tile, newest lowest: which runs are in the ring
-    uint32_t l_stage = 0;
-    auto issue = [&](bool any, bool next) {      // copies the cursor's tile and moves the cursor on
-        uint32_t row[2];
-        loaded <<= 2;
+    // the run of which this lane copies scales; none where there are fewer chunks than lanes
+    const int s_run = lane >= 2 * (kTile * C::kSRow / 16) ? -1 : (kOneRun ? 0 : (lane % (kTile * C::kSRow / 16)) / (kTile * C::kSRow / 32));
+    uint32_t loaded = 0;             // kRuns bits per tile, newest lowest: which runs are in the ring
+    const uint32_t ring_end = ring + C::kStages * C::kStageBytes;
+    auto issue = [&](uint32_t st) {              // copies the cursor's tile and moves on
+        if (l_at == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            row[i] = ((uint32_t)l_page[i] * (uint32_t)p.H_kv + (uint32_t)l_h) * (uint32_t)p.pg.page_size + (uint32_t)l_off[i];
-            if (l_page[i] >= 0) loaded |= 1u << i;
+            for (int i = 0; i < kRuns; ++i)
+                l_row[i] = (uint32_t)l_page[i] < (uint32_t)p.pg.num_pages
+                               ? ((uint32_t)l_page[i] * (uint32_t)p.H_kv + (uint32_t)l_h) * (uint32_t)p.pg.page_size + (uint32_t)l_off[i]
+                               : 0xffffffffu;
         }
-        const uint32_t st = ring + l_stage * C::kStageBytes;
-        if (any) {
+        uint32_t row[kRuns];
+        bool there[kRuns];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (l_page[i] >= 0) {
+        for (int i = 0; i < kRuns; ++i) {
+            row[i] = __shfl_sync(0xffffffffu, l_row[i], l_at);
+            there[i] = row[i] != 0xffffffffu;    // the same for all lanes
+            loaded = loaded * 2 + (there[i] ? 1u : 0u);
+        }
 #pragma unroll
-                    for (int j = 0; j < C::kRow / 32; ++j) {     // 16 keys: kRow / 32 chunks a lane
-                        cp_async16(st + dst_k + i * 16 * C::kRow + j * 512, src_k + (size_t)row[i] * C::kRow + j * 512);
-                        cp_async16(st + dst_v + i * 16 * C::kRow + j * 512, src_v + (size_t)row[i] * C::kRow + j * 512);
-                    }
+        for (int i = 0; i < kRuns; ++i)
+            if (there[i]) {
+                const uint8_t* const k = src_k + (size_t)row[i] * C::kRow;
+                const uint8_t* const v = src_v + (size_t)row[i] * C::kRow;
+#pragma unroll
+                for (int j = 0; j < 2 / kRuns * (C::kRow / 32); ++j) {   // 16 keys: kRow / 32 chunks a lane
+                    cp_async16(st + dst_k + i * 16 * C::kRow + j * 512, k + j * 512);
+                    cp_async16(st + dst_v + i * 16 * C::kRow + j * 512, v + j * 512);
                 }
-            const int page = s_second ? l_page[1] : l_page[0];
-            if (page >= 0 && lane < 2 * (kTile * C::kSRow / 16))
-                cp_async16(st + dst_s, src_s + (size_t)(s_second ? row[1] : row[0]) * C::kSRow);
-        }
+                if (s_run == i) cp_async16(st + dst_s, src_s + (size_t)row[i] * C::kSRow);
+            }
         cp_async_commit();
-        l_stage = l_stage + 1 == C::kStages ? 0 : l_stage + 1;
-        if (next) {
-            l_pos += kUnit;
-            if (--l_left == 0) {                 // the next item: next head, or next entry
+        ++l_at;
+        if (--l_left == 0) {                     // the next item: next head, or next entry
+            l_left = 0x7fffffff;
+            if (l_u + l_at < u1) {               // (behind the share nothing more is there)
                 if (++l_h == p.H_kv) {
                     l_h = 0;
                     const Entry y = entry_of<RB>(p, ++l_e);
@@ -344,16 +363,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     l_lo = y.lo + warp * kTile;
                     l_hi = y.hi;
                     l_b = y.b;
+                    if (l_table != nullptr) l_table = p.pg.table + (long long)l_b * p.pg.max_pages;
                 }
                 l_left = l_units;
                 l_pos = l_lo;
             }
+            look_up();
+        } else if (l_at == 32) {
+            l_pos += 32 * kUnit;
+            look_up();
         }
-        look_up(next);
     };
-    look_up(true);
+    look_up();
 #pragma unroll
-    for (int s = 0; s < C::kStages; ++s) issue(u0 + s < u1, u0 + s + 1 < u1);
+    for (int s = 0; s < C::kStages; ++s) issue(ring + s * C::kStageBytes);
 
     // ------------------------------------------------ state of the block's rows
     constexpr int kKW = D / 32;      // words of a key's codes per thread (a quarter of the row)
@@ -365,8 +388,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     float ref[NB][2];                // reference max of rows 2t, 2t + 1 (log2 units), equal in all lanes of a t
     float top[NB][2];                // raw score above which the reference moves
     float neg[NB][2];                // -ref, or 0 while the row has seen no key
-    uint32_t qf[NB == 1 ? D / 16 : 1][2];
-    const uint32_t qs = base + C::kQOff;
+    const uint32_t qs = base + C::kQOff + lane * 16;
     // MMA row i of a 16-key tile (i < 8) is key i/2 + 4 (i mod 2), row 8 + i that key + 8
     const int key0 = (g >> 1) + 4 * (g & 1);
     const uint32_t at_k = (uint32_t)((D == 128 ? key0 ^ ((key0 >> 2) & 1) : key0 ^ (((key0 >> 2) & 1) << 1)) * C::kRow +
@@ -378,37 +400,204 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     const uint32_t at_vs = C::kVSOff + (uint32_t)(t * C::kSRow + (g * (D / 8) / kGroup) * 2);
     const float inv_scale = 1.f / p.scale_log2;
 
-    uint32_t c_stage = 0;
+    uint32_t st = ring;              // the stage of the tile to take next
+    // A tile of 32 keys; kEdge: not every row of the block sees all of them.
+    auto tile = [&](auto edge_tag, const int pos, const uint32_t have) {
+        constexpr bool edge = decltype(edge_tag)::value;
+        // which of its 16-key halves are in the ring, from the bits of its runs (the first run highest)
+        auto half_there = [&](int j) { return kOneRun ? true : ((have >> (1 - j)) & 1u) != 0; };
+        // ------------------------------------ scores of two 16-key tiles
+        float s[2][NB][4];
+        uint32_t w0[2][kKW], w1[2][kKW], s0[2], s1[2], z0[2], z1[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) s[j][nb][0] = s[j][nb][1] = s[j][nb][2] = s[j][nb][3] = 0.f;
+            lds_words<kKW>(st + at_k + j * 16 * C::kRow, w0[j]);
+            lds_words<kKW>(st + at_k + (j * 16 + 8) * C::kRow, w1[j]);
+            s0[j] = lds_u16(st + at_ks + j * 16 * C::kSRow);
+            s1[j] = lds_u16(st + at_ks + (j * 16 + 8) * C::kSRow);
+            s0[j] = __byte_perm(s0[j], s0[j], 0x1010);
+            s1[j] = __byte_perm(s1[j], s1[j], 0x1010);
+            z0[j] = minus_24(s0[j]);
+            z1[j] = minus_24(s1[j]);
+        }
+#pragma unroll
+        for (int w = 0; w < kKW; ++w) {
+            uint32_t b[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) lds_words<4>(qs + (nb * kKW + w) * 512, b[nb]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t a0 = codes_to_bf16x2(0, w0[j][w], s0[j], z0[j]), a1 = codes_to_bf16x2(0, w1[j][w], s1[j], z1[j]);
+                const uint32_t a2 = codes_to_bf16x2(1, w0[j][w], s0[j], z0[j]), a3 = codes_to_bf16x2(1, w1[j][w], s1[j], z1[j]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_bf16(s[j][nb], a0, a1, a2, a3, b[nb][0], b[nb][1]);
+                const uint32_t c0 = codes_to_bf16x2(2, w0[j][w], s0[j], z0[j]), c1 = codes_to_bf16x2(2, w1[j][w], s1[j], z1[j]);
+                const uint32_t c2 = codes_to_bf16x2(3, w0[j][w], s0[j], z0[j]), c3 = codes_to_bf16x2(3, w1[j][w], s1[j], z1[j]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_bf16(s[j][nb], c0, c1, c2, c3, b[nb][2], b[nb][3]);
+            }
+        }
+        // ------------------------------------ mask, reference max, probabilities
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int r = nb * 8 + 2 * t + (c & 1), key = pos + 16 * j + key0 + (c >> 1) * 8;
+                        if (key < row_lo[r] || key >= row_hi[r] || !half_there(j)) s[j][nb][c] = -INFINITY;
+                    }
+        }
+        // the reference moves only when some score exceeds it by more than 2^8: until
+        // then probabilities stay below 2^8 and nothing needs to be rescaled
+        bool grow = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                grow |= fmaxf(max3f(s[0][nb][c], s[0][nb][c + 2], s[1][nb][c]), s[1][nb][c + 2]) > top[nb][c];
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float m = fmaxf(max3f(s[0][nb][c], s[0][nb][c + 2], s[1][nb][c]), s[1][nb][c + 2]) * p.scale_log2;
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m > ref[nb][c]) {
+                        const float f = ex2_approx(ref[nb][c] - m);   // 0 from a reference of -inf
+                        ref[nb][c] = m;
+                        neg[nb][c] = -m;
+                        top[nb][c] = (m + 8.f) * inv_scale;
+                        sum[nb][c] *= f;
+                        sumr[nb][c] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            acc[nb][mt][c] *= f;
+                            acc[nb][mt][c + 2] *= f;
+                        }
+                    }
+                }
+        }
+        uint32_t pb[2][NB][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float p0 = ex2_approx(fmaf(s[j][nb][0], p.scale_log2, neg[nb][0]));
+                const float p1 = ex2_approx(fmaf(s[j][nb][1], p.scale_log2, neg[nb][1]));
+                const float p2 = ex2_approx(fmaf(s[j][nb][2], p.scale_log2, neg[nb][0]));
+                const float p3 = ex2_approx(fmaf(s[j][nb][3], p.scale_log2, neg[nb][1]));
+                sum[nb][0] += p0 + p2;
+                sum[nb][1] += p1 + p3;
+                // P rounds to bf16 (2^-8) for the tensor cores; O is divided by the sum of
+                // the rounded values, so a row that one key dominates stays exact
+                pb[j][nb][0] = transpose8x8(pack_bf16x2(p0, p1));
+                pb[j][nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+                mma_bf16(sumr[nb], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, pb[j][nb][0], pb[j][nb][1]);
+            }
+        // ------------------------------------ O^T += V^T P^T
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t w[4][kVW], sv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lds_words<kVW>(st + at_v + (j * 16 + 4 * i) * C::kRow, w[i]);
+                sv[i] = lds_u16(st + at_vs + (j * 16 + 4 * i) * C::kSRow);
+            }
+            bool poisoned = false;
+            if (edge) {
+                // what lies behind the last key, or was not loaded, counts as zero; a NaN
+                // group of another key meets zero weights in the rows that do not see
+                // it: the tile is then taken row by row, with the hidden keys' scales zero
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (pos + 16 * j + t + 4 * i >= x.kl || !half_there(j)) sv[i] = 0;
+                    bad |= (sv[i] & 0x7fffu) > 0x7f80u;
+                }
+                poisoned = __any_sync(0xffffffffu, bad);
+            }
+            if (!poisoned) {
+                const uint32_t sA = __byte_perm(sv[0], sv[1], 0x5410), sB = __byte_perm(sv[2], sv[3], 0x5410);
+                const uint32_t zA = minus_24(sA), zB = minus_24(sB);
+#pragma unroll
+                for (int vw = 0; vw < kVW; ++vw) {
+                    const uint32_t la = __byte_perm(w[0][vw], w[1][vw], 0x5410);
+                    const uint32_t ha = __byte_perm(w[0][vw], w[1][vw], 0x7632);
+                    const uint32_t lb = __byte_perm(w[2][vw], w[3][vw], 0x5410);
+                    const uint32_t hb = __byte_perm(w[2][vw], w[3][vw], 0x7632);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = codes_to_bf16x2(i, la, sA, zA), a1 = codes_to_bf16x2(i, ha, sA, zA);
+                        const uint32_t a2 = codes_to_bf16x2(i, lb, sB, zB), a3 = codes_to_bf16x2(i, hb, sB, zB);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma_bf16(acc[nb][4 * vw + i], a0, a1, a2, a3, pb[j][nb][0], pb[j][nb][1]);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < RB; ++r) {
+                    uint32_t sr[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = pos + 16 * j + t + 4 * i;
+                        sr[i] = key >= row_lo[r] && key < row_hi[r] ? sv[i] : 0u;
+                    }
+                    const uint32_t sA = __byte_perm(sr[0], sr[1], 0x5410), sB = __byte_perm(sr[2], sr[3], 0x5410);
+                    const uint32_t zA = minus_24(sA), zB = minus_24(sB);
+#pragma unroll
+                    for (int vw = 0; vw < kVW; ++vw) {
+                        const uint32_t la = __byte_perm(w[0][vw], w[1][vw], 0x5410);
+                        const uint32_t ha = __byte_perm(w[0][vw], w[1][vw], 0x7632);
+                        const uint32_t lb = __byte_perm(w[2][vw], w[3][vw], 0x5410);
+                        const uint32_t hb = __byte_perm(w[2][vw], w[3][vw], 0x7632);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = codes_to_bf16x2(i, la, sA, zA), a1 = codes_to_bf16x2(i, ha, sA, zA);
+                            const uint32_t a2 = codes_to_bf16x2(i, lb, sB, zB), a3 = codes_to_bf16x2(i, hb, sB, zB);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float one[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_bf16(one, a0, a1, a2, a3, pb[j][nb][0], pb[j][nb][1]);
+                                // (selected, not indexed by r: acc stays in registers)
+                                const bool m0 = r == nb * 8 + 2 * t, m1 = r == nb * 8 + 2 * t + 1;
+                                acc[nb][4 * vw + i][0] += m0 ? one[0] : 0.f;
+                                acc[nb][4 * vw + i][1] += m1 ? one[1] : 0.f;
+                                acc[nb][4 * vw + i][2] += m0 ? one[2] : 0.f;
+                                acc[nb][4 * vw + i][3] += m1 ? one[3] : 0.f;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    };
+
     for (int u = u0; u < u1;) {
         // ============================================ a segment: units seg_k .. of an item
         const int n = min(x.units - seg_k, u1 - u);
         const int item_first = pre[seg_e] + seg_h * x.units;
         const bool whole = seg_k == 0 && n == x.units;
         unsigned long long* const word = p.words + (long long)seg_e * p.H_kv + seg_h;
-        if (!whole && tid == 0) arrive_claim(word, p.ticket);
+        unsigned long long found = 0;
+        if (!whole && tid == 0) found = arrive_claim(word, p.ticket);
         {
+            // Q as B fragments, two k-steps of the MMA to 16 bytes, shared by the warps
             const __nv_bfloat16* q = p.q + (((long long)x.b * p.H_kv + seg_h) * p.R + x.r0) * D;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (NB > 1 && warp != nb % kWarps) continue;     // one warp per 8 rows fills the shared copy
-                const int r = nb * 8 + g;
-                const uint4* src = reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4));
-#pragma unroll
-                for (int w = 0; w < kKW; ++w) {
-                    const uint4 y = r < x.nr ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-                    const uint32_t f[4] = {__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632),
-                                           __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632)};
-                    if constexpr (NB == 1) {
-                        qf[2 * w][0] = f[0];
-                        qf[2 * w][1] = f[1];
-                        qf[2 * w + 1][0] = f[2];
-                        qf[2 * w + 1][1] = f[3];
-                    } else {
-                        const uint32_t dst = qs + (uint32_t)(((nb * (D / 16) + 2 * w) * 32 + lane) * 8);
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(f[0]), "r"(f[1]) : "memory");
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + 256), "r"(f[2]), "r"(f[3]) : "memory");
-                    }
-                }
+            for (int i = warp; i < NB * kKW; i += kWarps) {
+                const int r = i / kKW * 8 + g, w = i % kKW;
+                const uint4 y = r < x.nr ? __ldg(reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4)) + w)
+                                         : make_uint4(0, 0, 0, 0);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qs + i * 512),
+                             "r"(__byte_perm(y.x, y.z, 0x5410)), "r"(__byte_perm(y.x, y.z, 0x7632)),
+                             "r"(__byte_perm(y.y, y.w, 0x5410)), "r"(__byte_perm(y.y, y.w, 0x7632))
+                             : "memory");
             }
         }
         if (tid < RB) {
@@ -436,196 +625,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             }
         }
         int pos = x.lo + seg_k * kUnit + warp * kTile;
+        const int full_hi = x.all_hi - kTile;
         for (int k = 0; k < n; ++k, ++u, pos += kUnit) {
             cp_async_wait<C::kStages - 1>();
             __syncwarp();
-            const uint32_t have = (loaded >> (2 * (C::kStages - 1))) & 3u;
-            const uint32_t st = ring + c_stage * C::kStageBytes;
-            if (have != 0) {
-                // ------------------------------------ scores of two 16-key tiles
-                float s[2][NB][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) s[j][nb][0] = s[j][nb][1] = s[j][nb][2] = s[j][nb][3] = 0.f;
-                    uint32_t w0[kKW], w1[kKW];
-                    lds_words<kKW>(st + at_k + j * 16 * C::kRow, w0);
-                    lds_words<kKW>(st + at_k + (j * 16 + 8) * C::kRow, w1);
-                    uint32_t s0 = lds_u16(st + at_ks + j * 16 * C::kSRow), s1 = lds_u16(st + at_ks + (j * 16 + 8) * C::kSRow);
-                    s0 = __byte_perm(s0, s0, 0x1010);
-                    s1 = __byte_perm(s1, s1, 0x1010);
-                    const uint32_t z0 = minus_24(s0), z1 = minus_24(s1);
-#pragma unroll
-                    for (int w = 0; w < kKW; ++w) {
-                        const uint32_t a0 = codes_to_bf16x2<0>(w0[w], s0, z0), a1 = codes_to_bf16x2<0>(w1[w], s1, z1);
-                        const uint32_t a2 = codes_to_bf16x2<1>(w0[w], s0, z0), a3 = codes_to_bf16x2<1>(w1[w], s1, z1);
-                        const uint32_t c0 = codes_to_bf16x2<2>(w0[w], s0, z0), c1 = codes_to_bf16x2<2>(w1[w], s1, z1);
-                        const uint32_t c2 = codes_to_bf16x2<3>(w0[w], s0, z0), c3 = codes_to_bf16x2<3>(w1[w], s1, z1);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            if constexpr (NB == 1) {
-                                mma_bf16(s[j][0], a0, a1, a2, a3, qf[2 * w][0], qf[2 * w][1]);
-                                mma_bf16(s[j][0], c0, c1, c2, c3, qf[2 * w + 1][0], qf[2 * w + 1][1]);
-                            } else {
-                                uint32_t b[2];
-                                lds_words<2>(qs + (uint32_t)(((nb * (D / 16) + 2 * w) * 32 + lane) * 8), b);
-                                mma_bf16(s[j][nb], a0, a1, a2, a3, b[0], b[1]);
-                                lds_words<2>(qs + (uint32_t)(((nb * (D / 16) + 2 * w + 1) * 32 + lane) * 8), b);
-                                mma_bf16(s[j][nb], c0, c1, c2, c3, b[0], b[1]);
-                            }
-                        }
-                    }
-                }
-                // ------------------------------------ mask, reference max, probabilities
-                const bool edge = pos < x.all_lo || pos + kTile > x.all_hi || have != 3;
-                if (edge) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int r = nb * 8 + 2 * t + (c & 1), key = pos + 16 * j + key0 + (c >> 1) * 8;
-                                if (key < row_lo[r] || key >= row_hi[r] || !((have >> j) & 1u)) s[j][nb][c] = -INFINITY;
-                            }
-                }
-                // the reference moves only when some score exceeds it by more than 2^8: until
-                // then probabilities stay below 2^8 and nothing needs to be rescaled
-                bool grow = false;
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        grow |= fmaxf(max3f(s[0][nb][c], s[0][nb][c + 2], s[1][nb][c]), s[1][nb][c + 2]) > top[nb][c];
-                if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float m = fmaxf(max3f(s[0][nb][c], s[0][nb][c + 2], s[1][nb][c]), s[1][nb][c + 2]) * p.scale_log2;
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                            if (m > ref[nb][c]) {
-                                const float f = ex2_approx(ref[nb][c] - m);   // 0 from a reference of -inf
-                                ref[nb][c] = m;
-                                neg[nb][c] = -m;
-                                top[nb][c] = (m + 8.f) * inv_scale;
-                                sum[nb][c] *= f;
-                                sumr[nb][c] *= f;
-#pragma unroll
-                                for (int mt = 0; mt < kMT; ++mt) {
-                                    acc[nb][mt][c] *= f;
-                                    acc[nb][mt][c + 2] *= f;
-                                }
-                            }
-                        }
-                }
-                uint32_t pb[2][NB][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        const float p0 = ex2_approx(fmaf(s[j][nb][0], p.scale_log2, neg[nb][0]));
-                        const float p1 = ex2_approx(fmaf(s[j][nb][1], p.scale_log2, neg[nb][1]));
-                        const float p2 = ex2_approx(fmaf(s[j][nb][2], p.scale_log2, neg[nb][0]));
-                        const float p3 = ex2_approx(fmaf(s[j][nb][3], p.scale_log2, neg[nb][1]));
-                        sum[nb][0] += p0 + p2;
-                        sum[nb][1] += p1 + p3;
-                        // P rounds to bf16 (2^-8) for the tensor cores; O is divided by the sum of
-                        // the rounded values, so a row that one key dominates stays exact
-                        pb[j][nb][0] = transpose8x8(pack_bf16x2(p0, p1));
-                        pb[j][nb][1] = transpose8x8(pack_bf16x2(p2, p3));
-                        mma_bf16(sumr[nb], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, pb[j][nb][0], pb[j][nb][1]);
-                    }
-                // ------------------------------------ O^T += V^T P^T
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t w[4][kVW], sv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        lds_words<kVW>(st + at_v + (j * 16 + 4 * i) * C::kRow, w[i]);
-                        sv[i] = lds_u16(st + at_vs + (j * 16 + 4 * i) * C::kSRow);
-                    }
-                    bool poisoned = false;
-                    if (edge) {
-                        // what lies behind the last key, or was not loaded, counts as zero; a NaN
-                        // group of another key meets zero weights in the rows that do not see
-                        // it: the tile is then taken row by row, with the hidden keys' scales zero
-                        bool bad = false;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (pos + 16 * j + t + 4 * i >= x.kl || !((have >> j) & 1u)) sv[i] = 0;
-                            bad |= (sv[i] & 0x7fffu) > 0x7f80u;
-                        }
-                        poisoned = __any_sync(0xffffffffu, bad);
-                    }
-                    if (!poisoned) {
-                        const uint32_t sA = __byte_perm(sv[0], sv[1], 0x5410), sB = __byte_perm(sv[2], sv[3], 0x5410);
-                        const uint32_t zA = minus_24(sA), zB = minus_24(sB);
-#pragma unroll
-                        for (int vw = 0; vw < kVW; ++vw) {
-                            const uint32_t la = __byte_perm(w[0][vw], w[1][vw], 0x5410);
-                            const uint32_t ha = __byte_perm(w[0][vw], w[1][vw], 0x7632);
-                            const uint32_t lb = __byte_perm(w[2][vw], w[3][vw], 0x5410);
-                            const uint32_t hb = __byte_perm(w[2][vw], w[3][vw], 0x7632);
-#define FA_KV4_PV(I)                                                                                       \
-    {                                                                                                      \
-        const uint32_t a0 = codes_to_bf16x2<I>(la, sA, zA), a1 = codes_to_bf16x2<I>(ha, sA, zA);           \
-        const uint32_t a2 = codes_to_bf16x2<I>(lb, sB, zB), a3 = codes_to_bf16x2<I>(hb, sB, zB);           \
-        _Pragma("unroll") for (int nb = 0; nb < NB; ++nb)                                                  \
-            mma_bf16(acc[nb][4 * vw + I], a0, a1, a2, a3, pb[j][nb][0], pb[j][nb][1]);                     \
-    }
-                            FA_KV4_PV(0)
-                            FA_KV4_PV(1)
-                            FA_KV4_PV(2)
-                            FA_KV4_PV(3)
-#undef FA_KV4_PV
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int r = 0; r < RB; ++r) {
-                            uint32_t sr[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int key = pos + 16 * j + t + 4 * i;
-                                sr[i] = key >= row_lo[r] && key < row_hi[r] ? sv[i] : 0u;
-                            }
-                            const uint32_t sA = __byte_perm(sr[0], sr[1], 0x5410), sB = __byte_perm(sr[2], sr[3], 0x5410);
-                            const uint32_t zA = minus_24(sA), zB = minus_24(sB);
-                            const bool mine0 = (r & 7) == 2 * t, mine1 = (r & 7) == 2 * t + 1;
-#pragma unroll
-                            for (int vw = 0; vw < kVW; ++vw) {
-                                const uint32_t la = __byte_perm(w[0][vw], w[1][vw], 0x5410);
-                                const uint32_t ha = __byte_perm(w[0][vw], w[1][vw], 0x7632);
-                                const uint32_t lb = __byte_perm(w[2][vw], w[3][vw], 0x5410);
-                                const uint32_t hb = __byte_perm(w[2][vw], w[3][vw], 0x7632);
-#define FA_KV4_PV_ROW(I)                                                                                   \
-    {                                                                                                      \
-        const uint32_t a0 = codes_to_bf16x2<I>(la, sA, zA), a1 = codes_to_bf16x2<I>(ha, sA, zA);           \
-        const uint32_t a2 = codes_to_bf16x2<I>(lb, sB, zB), a3 = codes_to_bf16x2<I>(hb, sB, zB);           \
-        _Pragma("unroll") for (int nb = 0; nb < NB; ++nb) {                                                \
-            float one[4] = {0.f, 0.f, 0.f, 0.f};                                                           \
-            mma_bf16(one, a0, a1, a2, a3, pb[j][nb][0], pb[j][nb][1]);                                     \
-            if (nb == (r >> 3)) {                                                                          \
-                if (mine0) acc[nb][4 * vw + I][0] += one[0], acc[nb][4 * vw + I][2] += one[2];             \
-                if (mine1) acc[nb][4 * vw + I][1] += one[1], acc[nb][4 * vw + I][3] += one[3];             \
-            }                                                                                              \
-        }                                                                                                  \
-    }
-                                FA_KV4_PV_ROW(0)
-                                FA_KV4_PV_ROW(1)
-                                FA_KV4_PV_ROW(2)
-                                FA_KV4_PV_ROW(3)
-#undef FA_KV4_PV_ROW
-                            }
-                        }
-                    }
-                }
-            }
+            const uint32_t have = (loaded >> (kRuns * (C::kStages - 1))) & ((1u << kRuns) - 1u);
+            if (pos >= x.all_lo && pos <= full_hi && have == (1u << kRuns) - 1u)
+                tile(std::false_type{}, pos, have);
+            else if (have != 0)
+                tile(std::true_type{}, pos, have);
             __syncwarp();                        // every lane has read the stage
-            c_stage = c_stage + 1 == C::kStages ? 0 : c_stage + 1;
-            issue(u + C::kStages < u1, u + C::kStages + 1 < u1);
+            issue(st);
+            st += C::kStageBytes;
+            if (st == ring_end) st = ring;
         }
 
         // -------------------------------------------- the segment's rows: combine the warps
@@ -648,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         __syncthreads();
         const int slot = (int)blockIdx.x * 2 + (u - n == u0 ? 0 : 1);
         const long long row0 = ((long long)x.b * p.H_kv + seg_h) * p.R + x.r0;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            if (nb * 8 < nr) {
+        auto combine = [&](auto block) {         // eight rows; a lambda, so that acc is indexed by constants
+            constexpr int nb = decltype(block)::value;
+            if (nb * 8 >= nr) return;
             if (nb > 0) __syncthreads();         // the exchange buffer is free again
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -703,8 +715,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                         *reinterpret_cast<float4*>(p.part_ml + ((long long)slot * RB + rr) * 4) = make_float4(m, lr, l, 0.f);
                 }
             }
-            }
-        }
+        };
+        combine(std::integral_constant<int, 0>{});
+        if constexpr (NB > 1) combine(std::integral_constant<int, 1>{});
         if (!whole) {
             // ---------------------------------------- partial: the last CTA of the item merges
             auto holder = [&](int v) {           // the CTA whose share has unit v
@@ -712,84 +725,113 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                 return v < big ? v / (each + 1) : more + (v - big) / each;
             };
             const int cf = holder(item_first), cl = holder(item_first + x.units - 1);
-            __threadfence();
             __syncthreads();
-            if (tid == 0) misc[0] = arrive_last(word, cl - cf + 1) ? 1 : 0;
+            if (tid == 0) {
+                __threadfence();                 // after the barrier: of all the CTA's writes
+                misc[0] = arrive_last(word, found, p.ticket, cl - cf + 1) ? 1 : 0;
+                __threadfence();
+            }
             __syncthreads();
             if (misc[0]) {
-                __threadfence();
                 // a CTA whose share starts inside the item has it first, else last: all but
                 // the first CTA have it first
                 const long long first = (long long)(2 * cf + (share(cf) >= item_first ? 0 : 1)) * RB;
                 auto at = [&](int c) { return c == cf ? first : (long long)(2 * c) * RB; };
-                // statistics of each row, a warp per row and a lane per CTA
+                // sums, 4 channels a thread; with few rows several threads share the CTAs of one.
+                // The first of them are on their way while the rows' statistics are made.
+                const int items = nr * (D / 4);
+                const int groups = items * 2 > kThreads ? 1 : kThreads / items;
+                constexpr int kAhead = 4;
+                float mc[kAhead];
+                float4 y[kAhead];
+                const int gi = groups == 1 ? 0 : tid / items;
+                const int rr0 = (tid - gi * items) / (D / 4), c40 = tid % (D / 4);
+                const bool in = gi < groups && rr0 < nr;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int c = cf + gi + i * groups;
+                    mc[i] = -INFINITY;
+                    y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in && c <= cl) {
+                        mc[i] = __ldcg(p.part_ml + (at(c) + rr0) * 4);
+                        y[i] = __ldcg(reinterpret_cast<const float4*>(p.part + (at(c) + rr0) * D) + c40);
+                    }
+                }
+                // statistics of each row: a warp per row, a lane per CTA
                 float* const fin = st_max;       // [RB] merged max, [RB] 1 / merged sum (the warps' own are used up)
                 for (int rr = warp; rr < nr; rr += kWarps) {
-                    float m = -INFINITY;
-                    for (int c = cf + lane; c <= cl; c += 32) m = fmaxf(m, __ldcg(p.part_ml + (at(c) + rr) * 4));
-#pragma unroll
-                    for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-                    float lr = 0.f, l = 0.f;
+                    float m = -INFINITY, lr = 0.f, l = 0.f;
                     for (int c = cf + lane; c <= cl; c += 32) {
                         const float4 ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(c) + rr) * 4));
-                        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-                        lr = fmaf(ml.y, f, lr);
-                        l = fmaf(ml.z, f, l);
+                        const float n = fmaxf(m, ml.x);
+                        const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
+                        const float h = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - n);
+                        lr = fmaf(lr, f, ml.y * h);
+                        l = fmaf(l, f, ml.z * h);
+                        m = n;
                     }
+                    float n = m;
+#pragma unroll
+                    for (int sh = 16; sh > 0; sh >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, sh));
+                    const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
+                    lr *= f;
+                    l *= f;
 #pragma unroll
                     for (int sh = 16; sh > 0; sh >>= 1) {
                         lr += __shfl_xor_sync(0xffffffffu, lr, sh);
                         l += __shfl_xor_sync(0xffffffffu, l, sh);
                     }
                     if (lane == 0) {
-                        fin[rr] = m;
+                        fin[rr] = n;
                         fin[RB + rr] = l == 0.f ? 0.f : 1.f / lr;
-                        p.lse[row0 + rr] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        p.lse[row0 + rr] = l == 0.f ? -INFINITY : (n + log2f(l)) * 0.69314718055994531f;
                     }
                 }
                 __syncthreads();
-                // sums, 4 channels a thread; with few rows several threads share the CTAs of one
-                const int items = nr * (D / 4);
-                const int groups = items * 2 > kThreads ? 1 : kThreads / items;
-                const bool in = groups == 1 || tid < items * groups;
-                for (int it = in ? tid : items; it < items * groups; it += kThreads) {
-                    const int gi = it / items, i = it - gi * items, rr = i / (D / 4), c4 = i % (D / 4);
+                auto add = [](float4& a, float m, float ref, const float4& v) {
+                    const float f = m == -INFINITY ? 0.f : ex2_approx(m - ref);
+                    a.x = fmaf(v.x, f, a.x);
+                    a.y = fmaf(v.y, f, a.y);
+                    a.z = fmaf(v.z, f, a.z);
+                    a.w = fmaf(v.w, f, a.w);
+                };
+                auto put = [&](int rr, int c4, const float4& a) {
+                    const float inv = fin[RB + rr];
+                    uint2 pk;
+                    pk.x = pack_bf16x2(a.x * inv, a.y * inv);
+                    pk.y = pack_bf16x2(a.z * inv, a.w * inv);
+                    *reinterpret_cast<uint2*>(p.o + (row0 + rr) * D + 4 * c4) = pk;
+                };
+                auto rest = [&](float4& a, int c, int rr, int c4) {
                     const float m = fin[rr];
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                    for (int c = cf + gi; c <= cl; c += groups) {
-                        const float mc = __ldcg(p.part_ml + (at(c) + rr) * 4);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + (at(c) + rr) * D) + c4);
-                        const float f = mc == -INFINITY ? 0.f : ex2_approx(mc - m);
-                        a.x = fmaf(y.x, f, a.x);
-                        a.y = fmaf(y.y, f, a.y);
-                        a.z = fmaf(y.z, f, a.z);
-                        a.w = fmaf(y.w, f, a.w);
-                    }
-                    if (groups > 1) {
-                        *reinterpret_cast<float4*>(red + it * 4) = a;
-                    } else {
-                        const float inv = fin[RB + rr];
-                        uint2 pk;
-                        pk.x = pack_bf16x2(a.x * inv, a.y * inv);
-                        pk.y = pack_bf16x2(a.z * inv, a.w * inv);
-                        *reinterpret_cast<uint2*>(p.o + (row0 + rr) * D + 4 * c4) = pk;
-                    }
+                    for (; c <= cl; c += groups)
+                        add(a, __ldcg(p.part_ml + (at(c) + rr) * 4), m,
+                            __ldcg(reinterpret_cast<const float4*>(p.part + (at(c) + rr) * D) + c4));
+                };
+                float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) add(a0, mc[i], fin[rr0], y[i]);
+                    rest(a0, cf + gi + kAhead * groups, rr0, c40);
                 }
-                if (groups > 1) {
+                if (groups == 1) {
+                    if (in) put(rr0, c40, a0);
+                    for (int it = tid + kThreads; it < items; it += kThreads) {
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                        rest(a, cf, it / (D / 4), it % (D / 4));
+                        put(it / (D / 4), it % (D / 4), a);
+                    }
+                } else {
+                    if (in) *reinterpret_cast<float4*>(red + tid * 4) = a0;
                     __syncthreads();
                     if (tid < items) {
-                        const int rr = tid / (D / 4), c4 = tid % (D / 4);
                         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int gi = 0; gi < groups; ++gi) {
-                            const float4 y = *reinterpret_cast<const float4*>(red + (gi * items + tid) * 4);
-                            a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+                        for (int i = 0; i < groups; ++i) {
+                            const float4 v = *reinterpret_cast<const float4*>(red + (i * items + tid) * 4);
+                            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
                         }
-                        const float inv = fin[RB + rr];
-                        uint2 pk;
-                        pk.x = pack_bf16x2(a.x * inv, a.y * inv);
-                        pk.y = pack_bf16x2(a.z * inv, a.w * inv);
-                        *reinterpret_cast<uint2*>(p.o + (row0 + rr) * D + 4 * c4) = pk;
+                        put(rr0, c40, a);
                     }
                 }
             }

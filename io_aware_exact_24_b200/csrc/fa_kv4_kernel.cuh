@@ -33,19 +33,22 @@ struct Paging {
     int num_pages;
     int page_size;            // a multiple of 16
     int max_pages;
-    uint32_t magic;           // floor((2^32 - 1) / page_size)
+    uint32_t magic, shift;    // n / page_size = umulhi(n, magic) >> shift for n < 2^31 (see divisor)
 };
 
-// n / page_size and the remainder: the reciprocal's quotient is the quotient or one less.
+// Exact division by d (16 <= d <= 2^31) of n < 2^31: with k = ceil(log2 d) and
+// m = ceil(2^(31+k) / d) < 2^32 + 1, n m / 2^(31+k) exceeds n / d by less than
+// n / 2^(31+k) <= 1 / d, which never reaches the next whole number.
+inline void divisor(uint32_t d, uint32_t& magic, uint32_t& shift) {
+    uint32_t k = 0;
+    while ((1ull << k) < d) ++k;
+    magic = (uint32_t)(((1ull << (31 + k)) + d - 1) / d);
+    shift = k - 1;
+}
 __device__ __forceinline__ int page_div(const Paging& pg, int n, int& rem) {
-    uint32_t q = __umulhi((uint32_t)n, pg.magic);
-    uint32_t r = (uint32_t)n - q * (uint32_t)pg.page_size;
-    if (r >= (uint32_t)pg.page_size) {
-        ++q;
-        r -= (uint32_t)pg.page_size;
-    }
-    rem = (int)r;
-    return (int)q;
+    const int q = (int)(__umulhi((uint32_t)n, pg.magic) >> pg.shift);
+    rem = n - q * pg.page_size;
+    return q;
 }
 
 // Page number of the p-th page of sequence b (p < max_pages); -1 if the table names none.
@@ -63,12 +66,12 @@ __device__ __forceinline__ int clamped(const int32_t* p, int b, int top) {
 }
 
 // ---------------------------------------------------------------- codes to bf16
-// The code at bits 4i..4i+3 of each half of w, as the bf16 pair (c - 8) * s: bits 3..6 of
+// The code at bits 4i .. 4i+3 of each half of w, as the bf16 pair (c - 8) * s: bits 3..6 of
 // a bf16 with the exponent of 16 weigh 8, 4, 2, 1, so the code placed there reads 16 + c,
 // and (16 + c) * s - 24 * s is exact (5 + 5 bits, then 5 significant bits of 24 s).
-template <int I>
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t w, uint32_t s2, uint32_t m24s2) {
-    uint32_t t = I == 0 ? w << 3 : w >> (I == 0 ? 0 : 4 * I - 3);
+// i is a constant wherever this is called.
+__device__ __forceinline__ uint32_t codes_to_bf16x2(int i, uint32_t w, uint32_t s2, uint32_t m24s2) {
+    uint32_t t = i == 0 ? w << 3 : w >> (4 * i - 3);
     asm("lop3.b32 %0, %0, 0x00780078, 0x41804180, 0xEA;" : "+r"(t));   // (t & mask) | 16.0
     uint32_t r;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(t), "r"(s2), "r"(m24s2));
@@ -183,8 +186,8 @@ struct ReadParams {
 
 __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t scale) {
     const uint32_t s2 = scale | (scale << 16), z2 = minus_24(s2);
-    const uint32_t a = codes_to_bf16x2<0>(w, s2, z2), b = codes_to_bf16x2<1>(w, s2, z2);   // channels (0,4), (1,5)
-    const uint32_t c = codes_to_bf16x2<2>(w, s2, z2), d = codes_to_bf16x2<3>(w, s2, z2);   // (2,6), (3,7)
+    const uint32_t a = codes_to_bf16x2(0, w, s2, z2), b = codes_to_bf16x2(1, w, s2, z2);   // channels (0,4), (1,5)
+    const uint32_t c = codes_to_bf16x2(2, w, s2, z2), d = codes_to_bf16x2(3, w, s2, z2);   // (2,6), (3,7)
     return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632),
                       __byte_perm(c, d, 0x7632));
 }

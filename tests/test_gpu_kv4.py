@@ -400,6 +400,25 @@ def test_bad_pages_are_masked():
     check(c, bits, [-3], None, 0.125, False, -1, o, lse)
 
 
+def test_a_cache_without_pages_is_empty():
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
+    B, H, H_kv, N, d = 2, 4, 2, 3, 64
+    (k, v), _ = tokens(B, H_kv, N, d, 38)
+    lens, none = ints([3, 3]), (None,) * 4
+    for table, maxp in ((None, 0), (None, 4), (ints([[0] * 4] * B), 4)):
+        fa_kv4_append(k, v, *none, table, lens, None, B, H_kv, N, d, 0, 16, maxp)
+        kb, vb = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+        fa_kv4_read(*none, table, lens, None, kb, vb, B, H_kv, N, d, 0, 16, maxp)
+        q = torch.ones((B, H, N, d), dtype=torch.bfloat16, device="cuda")
+        o, lse = torch.full_like(q, 7.0), torch.full((B, H, N), 7.0, device="cuda")
+        n = fa_fwd_kv4_workspace_size(B, H, H_kv, N, d)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        fa_fwd_kv4(q, *none, table, lens, None, o, lse, B, H, H_kv, N, d, 0, 16, maxp, 0.1, True, -1, ws, n)
+        torch.cuda.synchronize()
+        assert (kb == 0).all() and (vb == 0).all() and (o == 0).all() and torch.isneginf(lse).all()
+
+
 def test_more_sequences_than_one_launch_takes():
     import torch
     B = 1500
