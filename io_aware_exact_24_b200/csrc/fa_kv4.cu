@@ -59,11 +59,16 @@ kv4::Paging paging(const int32_t* table, int num_pages, int page_size, int max_p
     return pg;
 }
 
-// Grid of one thread per 8 channels of `rows` rows; false if it exceeds the launch limits.
-bool row_grid(long long rows, int d, unsigned* blocks) {
-    const long long per = 256 / (d / 8), n = (rows + per - 1) / per;
-    *blocks = (unsigned)n;
-    return n <= 0x7fffffffLL;
+// Launch of the kernels that write and read tokens (see kv4::kRowsPerThread); false if B * H_kv
+// exceeds the launch limits.
+bool row_grid(int B, int H_kv, int N, int d, dim3* grid, bool* flat, uint32_t* rows) {
+    const long long block = kv4::kRowThreads / (d / 8), per = block * kv4::kRowsPerThread, heads = (long long)B * H_kv;
+    if (heads > 0x7fffffffLL) return false;
+    *flat = N < per && heads * N <= 0x7fffffffLL;
+    *rows = *flat ? (uint32_t)(heads * N) : 0;
+    *grid = *flat ? dim3((unsigned)((heads * N + block - 1) / block))
+                  : dim3((unsigned)heads, (unsigned)std::min<long long>((N + per - 1) / per, kv4::kMaxRowBlocks));
+    return true;
 }
 
 // A 48-bit ticket other than 0 for each attention launch (see kv4::arrive_last).
@@ -152,17 +157,16 @@ int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, v
     p.pg = paging(block_table, num_pages, page_size, max_pages);
     p.H_kv = H_kv;
     p.N = N_new;
-    p.rows = (long long)B * H_kv * N_new;
-    unsigned blocks = 0;
-    if (!row_grid(p.rows, d, &blocks)) return FA_ERR_UNSUPPORTED;
+    dim3 grid;
+    bool flat = false;
+    if (!row_grid(B, H_kv, N_new, d, &grid, &flat, &p.rows)) return FA_ERR_UNSUPPORTED;
     int dev = -1, sms = 0;
     st = ready_device(&dev, &sms);
     if (st != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64)
-        kv4::append_kernel<64><<<blocks, 256, 0, s>>>(p);
-    else
-        kv4::append_kernel<128><<<blocks, 256, 0, s>>>(p);
+    const auto kernel = d == 64 ? (flat ? kv4::append_kernel<64, true> : kv4::append_kernel<64, false>)
+                                : (flat ? kv4::append_kernel<128, true> : kv4::append_kernel<128, false>);
+    kernel<<<grid, kv4::kRowThreads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache append)", e);
 }
@@ -188,17 +192,16 @@ int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, 
     p.pg = paging(block_table, num_pages, page_size, max_pages);
     p.H_kv = H_kv;
     p.N = N;
-    p.rows = (long long)B * H_kv * N;
-    unsigned blocks = 0;
-    if (!row_grid(p.rows, d, &blocks)) return FA_ERR_UNSUPPORTED;
+    dim3 grid;
+    bool flat = false;
+    if (!row_grid(B, H_kv, N, d, &grid, &flat, &p.rows)) return FA_ERR_UNSUPPORTED;
     int dev = -1, sms = 0;
     st = ready_device(&dev, &sms);
     if (st != FA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64)
-        kv4::read_kernel<64><<<blocks, 256, 0, s>>>(p);
-    else
-        kv4::read_kernel<128><<<blocks, 256, 0, s>>>(p);
+    const auto kernel = d == 64 ? (flat ? kv4::read_kernel<64, true> : kv4::read_kernel<64, false>)
+                                : (flat ? kv4::read_kernel<128, true> : kv4::read_kernel<128, false>);
+    kernel<<<grid, kv4::kRowThreads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache read)", e);
 }
