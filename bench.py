@@ -43,6 +43,7 @@ L2_FLUSH_BYTES = 256 << 20
 KERNEL_SOURCES = ["io_aware_exact_24_b200/csrc/fa_fwd_kernel.cuh",
                   "io_aware_exact_24_b200/csrc/fa_fwd_persist.cuh",
                   "io_aware_exact_24_b200/csrc/fa_decode_kernel.cuh",
+                  "io_aware_exact_24_b200/csrc/fa_kv4_rows.cuh",
                   "io_aware_exact_24_b200/csrc/sm100_ptx.cuh",
                   "io_aware_exact_24_b200/csrc/exp2_poly.cuh",
                   "io_aware_exact_24_b200/csrc/fa_api.cu"]

@@ -24,6 +24,7 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd_persist.cuh"
 #include "fa_decode_kernel.cuh"
+#include "fa_kv4_rows.cuh"
 
 // Dense forward launches use the persistent kernel (fa_fwd_persist.cuh); 0 keeps
 // one CTA per query block to the end (the split-KV and packed modes always do).
@@ -598,6 +599,38 @@ int ready_device(int* dev, int* num_sms) {
 }
 
 int current_num_sms() { return ::current_num_sms(); }
+
+namespace {
+template <int D, bool kOneRun>
+int launch_rows(const CUtensorMap& tq, const CUtensorMap& to, const fa::kv4::RowsParams& p, int B, cudaStream_t stream) {
+    constexpr int smem = fa::kv4::RowsCfg<D>::kSmemBytes;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t set[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kMaxDevices) return ::cuda_fail("cudaGetDevice", e);
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(fa::kv4::rows_kernel<D, kOneRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (set[dev] != cudaSuccess) return ::cuda_fail("cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", set[dev]);
+    const dim3 grid((unsigned)((p.rows.R + fa::kBlockM - 1) / fa::kBlockM), (unsigned)p.H_kv, (unsigned)B);
+    fa::kv4::rows_kernel<D, kOneRun><<<grid, fa::kv4::kRowThreads512, smem, stream>>>(tq, to, p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? FA_OK : ::cuda_fail("kernel launch (4-bit cache attention, many rows)", e);
+}
+}  // namespace
+
+int launch_kv4_rows(const void* q, void* o, int B, int d, fa::kv4::RowsParams p, cudaStream_t stream) {
+    CUtensorMap tq, to;
+    if (!encode_bhnd(&tq, q, B, p.H_kv, p.rows.R, d) || !encode_bhnd(&to, o, B, p.H_kv, p.rows.R, d)) {
+        snprintf(t_last_error, sizeof t_last_error, "cuTensorMapEncodeTiled failed");
+        return FA_ERR_CUDA;
+    }
+    p.wait_limit = kWaitLimitCycles;
+    const bool one = p.pg.page_size % 32 == 0;
+    if (d == 64) return one ? launch_rows<64, true>(tq, to, p, B, stream) : launch_rows<64, false>(tq, to, p, B, stream);
+    return one ? launch_rows<128, true>(tq, to, p, B, stream) : launch_rows<128, false>(tq, to, p, B, stream);
+}
 
 }  // namespace fa_internal
 

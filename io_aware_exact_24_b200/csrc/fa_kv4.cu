@@ -14,6 +14,9 @@
 #include "fa_kv4_attend.cuh"
 #include "fa_kv4_kernel.cuh"
 
+#ifndef FA_ROWS_MIN
+#define FA_ROWS_MIN 33
+#endif
 namespace {
 
 using fa_internal::cuda_fail;
@@ -238,6 +241,28 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
     if (st == FA_OK) st = prepare_attend(dev);
     if (st != FA_OK) return st;
+    kv4::Rows rows{};
+    rows.key_lens = key_lens;
+    rows.q_lens = q_lens;
+    rows.N_q = N_q;
+    rows.R = (int)R;
+    rows.causal = causal ? 1 : 0;
+    rows.window = window_left < 0 ? -1 : window_left;
+    const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R >= FA_ROWS_MIN) {
+        kv4::RowsParams p{};
+        p.k_codes = static_cast<const uint8_t*>(k_codes);
+        p.k_scales = static_cast<const uint16_t*>(k_scales);
+        p.v_codes = static_cast<const uint8_t*>(v_codes);
+        p.v_scales = static_cast<const uint16_t*>(v_scales);
+        p.pg = pg;
+        p.rows = rows;
+        p.H_kv = H_kv;
+        p.lse = lse;
+        p.scale_log2 = scale_log2;
+        return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
+    }
     const int rb = row_block(R);
     kv4::AttendParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -245,18 +270,13 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     p.k_scales = static_cast<const uint16_t*>(k_scales);
     p.v_codes = static_cast<const uint8_t*>(v_codes);
     p.v_scales = static_cast<const uint16_t*>(v_scales);
-    p.key_lens = key_lens;
-    p.q_lens = q_lens;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.pg = paging(block_table, num_pages, page_size, max_pages);
+    p.pg = pg;
     p.H_kv = H_kv;
-    p.N_q = N_q;
-    p.R = (int)R;
+    p.rows = rows;
     p.row_blocks = (int)((R + rb - 1) / rb);
     p.scale_log2 = scale_log2;
-    p.causal = causal ? 1 : 0;
-    p.window = window_left < 0 ? -1 : window_left;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part = reinterpret_cast<float*>(ws + L.part);
     p.part_ml = reinterpret_cast<float*>(ws + L.ml);
@@ -264,7 +284,6 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     const long long entries = (long long)B * p.row_blocks;
     // the line of units of one launch stays within int
     const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     for (long long e0 = 0; e0 < entries; e0 += chunk) {
         p.b0 = (int)(e0 / p.row_blocks);
         p.rb0 = (int)(e0 % p.row_blocks);

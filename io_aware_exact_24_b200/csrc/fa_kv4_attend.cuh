@@ -33,23 +33,20 @@ constexpr int kUnit = kTile * kWarps;            // keys per CTA and step
 constexpr int kMaxEntries = 512;                 // (sequence, row block) pairs per launch
 
 struct AttendParams {
-    const __nv_bfloat16* q;    // [B, H_kv, R, D], R = G * N_q
+    const __nv_bfloat16* q;    // [B, H_kv, R, D]
     const uint8_t* k_codes;
     const uint16_t* k_scales;
     const uint8_t* v_codes;
     const uint16_t* v_scales;
-    const int32_t* key_lens;
-    const int32_t* q_lens;     // or NULL: N_q
     __nv_bfloat16* o;
     float* lse;
     Paging pg;
-    int H_kv, N_q, R;
+    Rows rows;
+    int H_kv;
     int row_blocks;            // per sequence and head
     int b0, rb0;               // sequence and row block of this launch's first entry
     int E;                     // entries of this launch, <= kMaxEntries
     float scale_log2;          // scale * log2(e)
-    int causal;
-    int window;                // < 0: none
     float* part;               // per CTA two partial results: [2][RB][D] sums and [2][RB][4] (max, sums)
     float* part_ml;
     unsigned long long* words; // arrival words [E, H_kv]
@@ -136,62 +133,19 @@ __device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned l
     return true;
 }
 
-// What an entry (sequence, row block) attends to.
-struct Entry {
-    int b;
-    int r0, nr;            // first row and rows of the block
-    int kl, ql;            // keys and queries of the sequence
-    int lo, hi;            // keys some row of the block sees: [lo, hi), lo rounded down to a multiple of kTile
-    int all_lo, all_hi;    // keys every row sees
-    int units;             // at least 1
-};
-
+// Entry e of a launch: its sequence and row block.
 template <int RB>
 __device__ __forceinline__ Entry entry_of(const AttendParams& p, int e) {
-    Entry x;
-    int g = p.rb0 + e;
-    x.b = p.b0;
+    int g = p.rb0 + e, b = p.b0;
     if (p.row_blocks == 1) {
-        x.b += g;
+        b += g;
         g = 0;
     } else {
         const int n = g / p.row_blocks;
-        x.b += n;
+        b += n;
         g -= n * p.row_blocks;
     }
-    x.r0 = g * RB;
-    x.nr = min(RB, p.R - x.r0);
-    x.kl = clamped(p.key_lens, x.b, p.pg.max_pages * p.pg.page_size);
-    x.ql = clamped(p.q_lens, x.b, p.N_q);
-    // the queries among the rows (row = head in group * N_q + query)
-    int i0 = 0, i1 = p.N_q - 1;
-    if (x.nr < p.N_q) {
-        const int a = x.r0 % p.N_q, z = a + x.nr - 1;
-        if (z < p.N_q) {
-            i0 = a;
-            i1 = z;
-        }
-    }
-    const bool rows_without = i1 >= x.ql;
-    i1 = min(i1, x.ql - 1);
-    const long long off = (long long)x.kl - x.ql;
-    long long lo = 0, hi = i0 > i1 ? 0 : x.kl, all_lo = 0, all_hi = rows_without ? 0 : x.kl;
-    if (p.causal) {
-        hi = min(hi, off + i1 + 1);
-        all_hi = min(all_hi, off + i0 + 1);
-    }
-    if (p.window >= 0) {
-        lo = max(lo, off + i0 - p.window);
-        all_lo = max(all_lo, off + i1 - p.window);
-    }
-    hi = max(hi, 0ll);
-    lo = min(lo, hi);
-    x.lo = (int)lo & ~(kTile - 1);
-    x.hi = (int)hi;
-    x.all_lo = (int)all_lo;
-    x.all_hi = (int)max(all_hi, 0ll);
-    x.units = max(1, (x.hi - x.lo + kUnit - 1) / kUnit);
-    return x;
+    return entry_of_rows<RB, kTile, kUnit>(p.rows, p.pg, b, g * RB);
 }
 
 template <int D, int NB, bool kOneRun>
@@ -589,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         if (!whole && tid == 0) found = arrive_claim(word, p.ticket);
         {
             // Q as B fragments, two k-steps of the MMA to 16 bytes, shared by the warps
-            const __nv_bfloat16* q = p.q + (((long long)x.b * p.H_kv + seg_h) * p.R + x.r0) * D;
+            const __nv_bfloat16* q = p.q + (((long long)x.b * p.H_kv + seg_h) * p.rows.R + x.r0) * D;
             for (int i = warp; i < NB * kKW; i += kWarps) {
                 const int r = i / kKW * 8 + g, w = i % kKW;
                 const uint4 y = r < x.nr ? __ldg(reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4)) + w)
@@ -601,13 +555,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             }
         }
         if (tid < RB) {
-            const int i = p.N_q == 1 ? 0 : (x.r0 + tid) % p.N_q;
-            const long long at = (long long)x.kl - x.ql + i;
-            long long lo = 0, hi = (tid < x.nr && i < x.ql) ? x.kl : 0;
-            if (p.causal) hi = min(hi, at + 1);
-            if (p.window >= 0) lo = max(lo, at - p.window);
-            row_lo[tid] = (int)min(lo, 0x7fffffffLL);
-            row_hi[tid] = (int)max(hi, 0LL);
+            int lo, hi;
+            row_keys(p.rows, x.kl, x.ql, x.r0 + tid, lo, hi);
+            row_lo[tid] = lo;
+            row_hi[tid] = hi;
         }
         __syncthreads();
 #pragma unroll
@@ -659,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             }
         __syncthreads();
         const int slot = (int)blockIdx.x * 2 + (u - n == u0 ? 0 : 1);
-        const long long row0 = ((long long)x.b * p.H_kv + seg_h) * p.R + x.r0;
+        const long long row0 = ((long long)x.b * p.H_kv + seg_h) * p.rows.R + x.r0;
         auto combine = [&](auto block) {         // eight rows; a lambda, so that acc is indexed by constants
             constexpr int nb = decltype(block)::value;
             if (nb * 8 >= nr) return;

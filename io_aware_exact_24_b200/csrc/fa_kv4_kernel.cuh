@@ -65,6 +65,90 @@ __device__ __forceinline__ int clamped(const int32_t* p, int b, int top) {
     return v < 0 ? 0 : (v > top ? top : v);
 }
 
+// ---------------------------------------------------------------- rows and what they see
+// All G = H / H_kv query heads of a key/value head, times N_q queries, are the rows that meet
+// its keys: row = head in group * N_q + query.
+struct Rows {
+    const int32_t* key_lens;
+    const int32_t* q_lens;     // or NULL: N_q
+    int N_q, R;                // R = G * N_q
+    int causal;
+    int window;                // < 0: none
+};
+
+// Keys [lo, hi) that a row of a sequence with kl keys and ql queries sees (hi <= lo: none).
+__device__ __forceinline__ void row_keys(const Rows& p, int kl, int ql, int row, int& lo, int& hi) {
+    const int i = p.N_q == 1 ? 0 : row % p.N_q;
+    const long long at = (long long)kl - ql + i;
+    long long l = 0, h = (row < p.R && i < ql) ? kl : 0;
+    if (p.causal) h = min(h, at + 1);
+    if (p.window >= 0) l = max(l, at - p.window);
+    lo = (int)min(l, 0x7fffffffLL);
+    hi = (int)max(h, 0LL);
+}
+
+// What a block of rows of a sequence attends to.
+struct Entry {
+    int b;
+    int r0, nr;            // first row and rows of the block
+    int kl, ql;            // keys and queries of the sequence
+    int lo, hi;            // keys some row of the block sees: [lo, hi), lo rounded down to a multiple of kTile
+    int all_lo, all_hi;    // keys every row sees
+    int units;             // of kUnit keys from lo, at least 1
+};
+
+template <int RB, int kTile, int kUnit>
+__device__ __forceinline__ Entry entry_of_rows(const Rows& p, const Paging& pg, int b, int r0) {
+    Entry x;
+    x.b = b;
+    x.r0 = r0;
+    x.nr = min(RB, p.R - r0);
+    x.kl = clamped(p.key_lens, b, pg.max_pages * pg.page_size);
+    x.ql = clamped(p.q_lens, b, p.N_q);
+    int i0 = 0, i1 = p.N_q - 1;              // the queries among the rows
+    if (x.nr < p.N_q) {
+        const int a = r0 % p.N_q, z = a + x.nr - 1;
+        if (z < p.N_q) {
+            i0 = a;
+            i1 = z;
+        }
+    }
+    const bool rows_without = i1 >= x.ql;
+    i1 = min(i1, x.ql - 1);
+    const long long off = (long long)x.kl - x.ql;
+    long long lo = 0, hi = i0 > i1 ? 0 : x.kl, all_lo = 0, all_hi = rows_without ? 0 : x.kl;
+    if (p.causal) {
+        hi = min(hi, off + i1 + 1);
+        all_hi = min(all_hi, off + i0 + 1);
+    }
+    if (p.window >= 0) {
+        lo = max(lo, off + i0 - p.window);
+        all_lo = max(all_lo, off + i1 - p.window);
+    }
+    hi = max(hi, 0ll);
+    lo = min(lo, hi);
+    x.lo = (int)lo & ~(kTile - 1);
+    x.hi = (int)hi;
+    x.all_lo = (int)all_lo;
+    x.all_hi = (int)max(all_hi, 0ll);
+    x.units = max(1, (x.hi - x.lo + kUnit - 1) / kUnit);
+    return x;
+}
+
+// Of the kernel for many rows (fa_kv4_rows.cuh).
+struct RowsParams {
+    const uint8_t* k_codes;
+    const uint16_t* k_scales;
+    const uint8_t* v_codes;
+    const uint16_t* v_scales;
+    Paging pg;
+    Rows rows;
+    int H_kv;
+    float* lse;                      // [B, H_kv, R]
+    float scale_log2;
+    unsigned long long wait_limit;
+};
+
 // ---------------------------------------------------------------- codes to bf16
 // The code at bits 4i .. 4i+3 of each half of w, as the bf16 pair (c - 8) * s: bits 3..6 of
 // a bf16 with the exponent of 16 weigh 8, 4, 2, 1, so the code placed there reads 16 + c,

@@ -1,0 +1,515 @@
+// fa_kv4_rows.cuh -- attention over the 4-bit paged cache for many query rows per key/value
+// head (pieces of prompts), on the tcgen05 tensor cores.
+//
+// The rows of a key/value head (fa_kv4_kernel.cuh: Rows) come in blocks of 128, one CTA each.
+// The kernel is the forward of fa_fwd_kernel.cuh (S = Q K^T and O += P V in TMEM, two softmax
+// warps per lane quadrant, the reference max that moves by 2^8) with another source of K and
+// V: four warps read the codes of a 128-key tile into registers, one tile ahead, turn them
+// into bf16 and store them to the swizzled tiles that the MMAs read.  The values are exact
+// (fa_kv4_kernel.cuh), so the tensor cores multiply what a read-back cache would hold, and no
+// bf16 copy of the cache passes through memory.
+//
+// The codes of a 32-bit word come out as channels (0,4) (1,5) (2,6) (3,7).  K is stored in
+// that order, Q is brought into it once per CTA, and of O, whose columns follow V's, the
+// epilogue picks the columns back.
+//
+// A NaN group of V would reach the rows that do not see its key as 0 * NaN: it is stored as
+// zeros and noted in a mask per tile, and the softmax threads, which know what their row sees,
+// make the group's channels NaN at the end.
+#pragma once
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_kv4_kernel.cuh"
+
+namespace fa {
+namespace kv4 {
+
+constexpr int kRowThreads512 = 512;          // 8 softmax warps, 4 control warps, 4 that make K and V tiles
+constexpr int kMakerWarp = 12;
+constexpr int kMakers = 4;
+// Registers per thread: 512 x 128 at launch; 2 x 128 x 184 + 128 x 48 + 128 x 96 are as many.
+constexpr uint32_t kRegsRowsSoftmax = 184;
+constexpr uint32_t kRegsRowsControl = 48;
+constexpr uint32_t kRegsRowsMaker = 96;
+// Tiles whose notes are kept.  A maker writes tile j's when the scores of tile j - stages are
+// done, so those of tile j - stages - 1 have been read, and with them its notes.
+constexpr int kNotes = 8;
+static_assert(kNotes > fa::Cfg<64>::kStagesK && kNotes > fa::Cfg<128>::kStagesK, "notes still to be read");
+
+template <int D>
+struct RowsCfg {
+    using F = fa::Cfg<D>;
+    // barriers: q_full, q_ready, then per ring full and empty, s_full[2], s_free, p_full[3], pv_done[3], drain
+    static constexpr int kNumBars = 2 + 2 * F::kStages + 2 + 1 + 3 + 3 + 1;
+    static constexpr int kBarOff = F::kBarOff;
+    static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // tmem base, abort flag
+    static constexpr int kMrefOff = kMiscOff + 16;
+    static constexpr int kEpiOff = kMrefOff + kGroups * kBlockM * 8;           // m, sum, NaN groups [2][row] each
+    // notes of a tile: a word per maker warp (bits 0-1: its runs that are not there, bit 2: NaN
+    // groups), then its 32 keys' NaN bits per group
+    static constexpr int kNoteBytes = kMakers * 4 * (1 + D / kGroup);
+    static constexpr int kNoteOff = kEpiOff + 3 * kGroups * kBlockM * 4;
+    static constexpr int kSmemBytes = kNoteOff + kNotes * kNoteBytes + 1024;
+    static_assert(kSmemBytes <= 232448 && kSmemBytes > 116 * 1024, "one CTA per SM");
+};
+
+// The pairs (0,1) (2,3) (4,5) (6,7) of 8 channels as (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ uint4 code_order(uint4 x) {
+    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                      __byte_perm(x.y, x.w, 0x7632));
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int D, bool kOneRun>
+__global__ void __launch_bounds__(kRowThreads512, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o, const RowsParams p) {
+    using F = fa::Cfg<D>;
+    using C = RowsCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_base = smem_addr(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* const base_ptr = smem_raw + (base - raw_base);
+
+    auto bar = [&](int i) { return base + C::kBarOff + 8u * (uint32_t)i; };
+    const uint32_t bar_q_full = bar(0), bar_q_ready = bar(1);
+    auto bar_full = [&](int r, int s) { return bar(2 + r * F::kStagesK + s); };
+    auto bar_empty = [&](int r, int s) { return bar(2 + F::kStages + r * F::kStagesK + s); };
+    auto bar_s_full = [&](int g) { return bar(2 + 2 * F::kStages + g); };
+    const uint32_t bar_s_free = bar(4 + 2 * F::kStages);
+    auto bar_p_full = [&](int b) { return bar(5 + 2 * F::kStages + b); };
+    auto bar_pv_done = [&](int b) { return bar(8 + 2 * F::kStages + b); };
+    const uint32_t bar_drain = bar(11 + 2 * F::kStages);
+    uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
+    const uint32_t mref_w = base + C::kMrefOff;
+    float* const epi = reinterpret_cast<float*>(base_ptr + C::kEpiOff);
+    const uint32_t q_tile = base + F::kQOff;
+    auto ring_slot = [&](int r, int s) {
+        return r == 0 ? base + F::kKOff + (uint32_t)(s * F::kTileBytes) : base + F::kVOff + (uint32_t)(s * F::kVSlotBytes);
+    };
+    auto note = [&](int j) { return reinterpret_cast<volatile uint32_t*>(base_ptr + C::kNoteOff + (j % kNotes) * C::kNoteBytes); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // rows that see more keys (causal: the later ones of a head) start first
+    const int m0 = (int)(gridDim.x - 1 - blockIdx.x) * kBlockM;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const Entry x = entry_of_rows<kBlockM, 32, kBlockN>(p.rows, p.pg, b, m0);
+    const int n_kv = x.hi > x.lo ? x.units : 0;
+
+    // ---- setup
+    if (warp == kProducerWarp && lane == 0) {
+        mbar_init(bar_q_full, 1);
+        mbar_init(bar_q_ready, kMakers);
+        for (int r = 0; r < 2; ++r)
+            for (int s = 0; s < (r == 0 ? F::kStagesK : F::kStagesV); ++s) {
+                mbar_init(bar_full(r, s), kMakers);
+                mbar_init(bar_empty(r, s), 1);
+            }
+        mbar_init(bar_s_full(0), 1);
+        mbar_init(bar_s_full(1), 1);
+        mbar_init(bar_s_free, 4);
+        for (int i = 0; i < F::kPBufs; ++i) {
+            mbar_init(bar_p_full(i), 4);
+            mbar_init(bar_pv_done(i), 1);
+        }
+        mbar_init(bar_drain, 2);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_o);
+    }
+    for (int i = threadIdx.x; i < kGroups * kBlockM; i += kRowThreads512) st_relaxed_shared_u64(mref_w + 8u * (uint32_t)i, ~0ull);
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(tmem_holder), kTmemCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    // the ones box of every V slot: the PV product's last columns sum the rounded P
+    for (int i = threadIdx.x; i < F::kStagesV * (F::kBoxBytes / 16); i += kRowThreads512) {
+        const uint32_t a = ring_slot(1, i / (F::kBoxBytes / 16)) + (uint32_t)F::kTileBytes + (uint32_t)(i % (F::kBoxBytes / 16)) * 16u;
+        sts16(a, F::kOnesWord, F::kOnesWord, F::kOnesWord, F::kOnesWord);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp >= kMakerWarp) {
+        setmaxnreg_dec<kRegsRowsMaker>();
+        // =========================================================== K and V tiles
+        // Warp w makes keys 32w .. 32w + 31 of each tile.  A lane takes one group of 32 channels
+        // (a scale, 16 bytes of codes) of a key: 8 (d = 128) or 16 keys of the same group lie in
+        // neighbouring lanes, which store to different banks.
+        constexpr int kG = D / kGroup, kKeys = 32 / kG, kPass = 32 / kKeys;
+        constexpr int kRuns = kOneRun ? 1 : 2;
+        const int w = warp - kMakerWarp;
+        const int key_l = lane % kKeys, grp = lane / kKeys;
+        bool ok = true;
+        int page[kRuns], off[kRuns];
+        auto look_up = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                const int pos = x.lo + j * kBlockN + w * 32 + 16 * i;
+                page[i] = -1;
+                off[i] = 0;
+                if (j < n_kv && pos < x.hi) page[i] = page_of(p.pg, b, page_div(p.pg, pos, off[i]));
+            }
+        };
+        uint4 kc[kPass], vc[kPass];
+        uint32_t sc[kPass];          // K's scale in the low half, V's in the high one
+        uint32_t vrow[kPass];        // V's row, ~0 where there is none
+        uint32_t gone = 0;           // runs of the loaded tile that are not there
+        // Tile j's K and all its scales; load_v then takes its V.  Each is on its way while
+        // the other tensor's tile is made.
+        auto load_k = [&](int j) {
+            gone = 0;
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) {
+                const int i = o * kKeys / 16 % kRuns, in = o * kKeys - (kOneRun ? 0 : i * 16);
+                kc[o] = make_uint4(0, 0, 0, 0);
+                sc[o] = 0;
+                vrow[o] = 0xffffffffu;
+                if (page[i] >= 0) {
+                    const uint32_t row = ((uint32_t)page[i] * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size +
+                                         (uint32_t)(off[i] + in + key_l);
+                    kc[o] = __ldg(reinterpret_cast<const uint4*>(p.k_codes + (size_t)row * (D / 2)) + grp);
+                    sc[o] = __ldg(p.k_scales + (size_t)row * kG + grp);
+                    vrow[o] = row;
+                    // rows behind the last key may hold anything: their V counts as zero
+                    if (x.lo + j * kBlockN + w * 32 + o * kKeys + key_l < x.kl)
+                        sc[o] |= (uint32_t)__ldg(p.v_scales + (size_t)row * kG + grp) << 16;
+                } else {
+                    gone |= kOneRun ? 3u : 1u << i;
+                }
+            }
+        };
+        auto load_v = [&]() {
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) {
+                vc[o] = make_uint4(0, 0, 0, 0);
+                if (vrow[o] != 0xffffffffu) vc[o] = __ldg(reinterpret_cast<const uint4*>(p.v_codes + (size_t)vrow[o] * (D / 2)) + grp);
+            }
+        };
+        auto store = [&](uint32_t slot, int o, const uint4& c, uint32_t s) {
+            const uint32_t s2 = __byte_perm(s, s, 0x1010), z2 = minus_24(s2);
+            const int key = w * 32 + o * kKeys + key_l;
+            const uint32_t at = slot + (uint32_t)((grp >> 1) * F::kBoxBytes + key * 128);
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sts16(at + (uint32_t)(((((grp & 1) << 2) + i) ^ (key & 7)) << 4), codes_to_bf16x2(0, cw[i], s2, z2),
+                      codes_to_bf16x2(1, cw[i], s2, z2), codes_to_bf16x2(2, cw[i], s2, z2), codes_to_bf16x2(3, cw[i], s2, z2));
+        };
+        if (n_kv > 0) {
+            look_up(0);
+            load_k(0);
+            load_v();
+            look_up(1);
+            // Q into the order of the codes: row 32w + lane
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_q_full, 0, abort_flag, p.wait_limit));
+            if (ok) {
+                const uint32_t row = q_tile + (uint32_t)(w * 32 + lane) * 128u;
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t a = row + (uint32_t)((i >> 3) * F::kBoxBytes + (((i & 7) ^ (lane & 7)) << 4));
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+                    v = code_order(v);
+                    sts16(a, v.x, v.y, v.z, v.w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_q_ready);
+            }
+        }
+        for (int j = 0; j < n_kv && ok; ++j) {
+            const int sk = j % F::kStagesK, sv = j % F::kStagesV;
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(0, sk), ((uint32_t)(j / F::kStagesK) & 1u) ^ 1u, abort_flag, p.wait_limit));
+            if (!ok) break;
+            // notes first: whoever sees this tile's scores sees them too
+            uint32_t bad = 0;
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) bad |= ((sc[o] >> 16) & 0x7f80u) == 0x7f80u ? 1u << o : 0u;
+            const bool any_bad = __any_sync(0xffffffffu, bad != 0);
+            if (any_bad) {
+                uint32_t word = 0;           // lane g's: the 32 keys' bits of group g
+#pragma unroll
+                for (int o = 0; o < kPass; ++o) {
+                    const uint32_t bal = __ballot_sync(0xffffffffu, (bad >> o) & 1u);
+                    if (lane < kG) word |= ((bal >> (lane * kKeys)) & ((1u << kKeys) - 1u)) << (o * kKeys);
+                    if ((bad >> o) & 1u) sc[o] &= 0xffffu;
+                }
+                if (lane < kG) note(j)[kMakers + w * kG + lane] = word;
+            }
+            if (lane == 0) note(j)[w] = gone | (any_bad ? 4u : 0u);
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sk), o, kc[o], sc[o]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_full(0, sk));
+            uint32_t sv2[kPass];
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) sv2[o] = sc[o] >> 16;
+            load_k(j + 1);
+            look_up(j + 2);
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(1, sv), ((uint32_t)(j / F::kStagesV) & 1u) ^ 1u, abort_flag, p.wait_limit));
+            if (!ok) break;
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sv), o, vc[o], sv2[o]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_full(1, sv));
+            load_v();
+        }
+        __syncwarp();
+    } else if (warp >= kProducerWarp) {
+        setmaxnreg_dec<kRegsRowsControl>();
+        if (warp == kProducerWarp) {
+            if (lane == 0 && n_kv > 0) {
+                mbar_arrive_expect_tx(bar_q_full, (uint32_t)F::kTileBytes);
+                for (int bx = 0; bx < F::kBoxes; ++bx)
+                    tma_load_4d(q_tile + bx * F::kBoxBytes, &tm_q, bar_q_full, bx * F::kBoxCols, m0, h, b, policy_evict_first());
+                (void)wait_own_work(bar_q_full, 0);   // the copy has landed before the CTA can exit
+            }
+        } else if (warp == kMmaWarp || warp == kPvWarp) {
+            // ======================================================= MMA issuers
+            if (lane == 0 && n_kv > 0) {
+                bool ok = true;
+                if (warp == kMmaWarp) {
+                    ok = wait_bounded(bar_q_ready, 0, abort_flag, p.wait_limit);
+                    for (int i = 0; i < n_kv && ok; ++i) {
+                        if (i > 0) ok = wait_bounded(bar_s_free, (uint32_t)((i - 1) & 1), abort_flag, p.wait_limit);
+                        const int sl = i % F::kStagesK;
+                        if (ok) ok = wait_bounded(bar_full(0, sl), (uint32_t)((i / F::kStagesK) & 1), abort_flag, p.wait_limit);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t slot = ring_slot(0, sl);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t koff = (uint32_t)((kk / 4) * F::kBoxBytes + (kk % 4) * 32);
+                            umma_ss(tmem + F::col_s(0), smem_desc_sw128(q_tile + koff, 16, 1024),
+                                    smem_desc_sw128(slot + koff, 16, 1024), F::kIdescQK, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(bar_s_full(i & 1));
+                        umma_commit(bar_empty(0, sl));
+                    }
+                } else {
+                    for (int j = 0; j < n_kv && ok; ++j) {
+                        const int pb = j % F::kPBufs, sl = j % F::kStagesV;
+                        ok = wait_bounded(bar_p_full(pb), (uint32_t)((j / F::kPBufs) & 1), abort_flag, p.wait_limit);
+                        if (ok) ok = wait_bounded(bar_full(1, sl), (uint32_t)((j / F::kStagesV) & 1), abort_flag, p.wait_limit);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t slot = ring_slot(1, sl);
+#pragma unroll
+                        for (int kk = 0; kk < kBlockN / 16; ++kk)
+                            umma_ts(tmem + F::kColO, tmem + F::col_p(pb) + (uint32_t)(kk * 8),
+                                    smem_desc_sw128(slot + (uint32_t)(kk * 16 * 128), F::kBoxBytes, 1024), F::kIdescPV,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(bar_pv_done(pb));
+                        umma_commit(bar_empty(1, sl));
+                    }
+                }
+                // every MMA and commit has landed before TMEM is freed, after an abort too
+                umma_commit(bar_drain);
+                (void)wait_own_work(bar_drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        setmaxnreg_inc<kRegsRowsSoftmax>();
+        // =========================================================== softmax: one thread per row, tiles in turn
+        const int qd = warp & 3, g = warp >> 2;
+        const int r = qd * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+        const int row = m0 + r;
+        int lo, lim;
+        row_keys(p.rows, x.kl, x.ql, row, lo, lim);
+        const float c = p.scale_log2;
+        float m_seen = -INFINITY, lu = 0.f;
+        uint32_t nan_groups = 0;         // groups of V that a key this row sees holds as NaN
+        bool ok = true;
+        for (int j = g; j < n_kv; j += 2) {
+            bool good = wait_bounded(bar_s_full(g), (uint32_t)((j >> 1) & 1), abort_flag, p.wait_limit);
+            if (!__all_sync(0xffffffffu, good)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int kbase = x.lo + j * kBlockN;
+            uint32_t notes = 0;          // bits 2w, 2w + 1: runs of warp w that are not there
+            uint32_t any_nan = 0;
+#pragma unroll
+            for (int w = 0; w < kMakers; ++w) {
+                const uint32_t n = note(j)[w];
+                notes |= (n & 3u) << (2 * w);
+                any_nan |= n & 4u;
+            }
+            if (any_nan) {
+                for (int w = 0; w < kMakers; ++w)
+                    if (note(j)[w] & 4u)
+                        for (int q = 0; q < D / kGroup; ++q) {
+                            const uint32_t bits = note(j)[kMakers + w * (D / kGroup) + q];
+                            for (int i = 0; i < 32; ++i) {
+                                const int key = kbase + w * 32 + i;
+                                if (((bits >> i) & 1u) && key >= lo && key < lim) nan_groups |= 1u << q;
+                            }
+                        }
+            }
+            float s[kBlockN];
+            {
+                uint32_t u[kBlockN];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+                    tmem_ld32(tmem + lane_off + F::col_s(0) + 32u * q4, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q4]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < kBlockN; ++i) {
+                    reg_after_wait(u[i]);
+                    s[i] = __uint_as_float(u[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_s_free);
+            if (__any_sync(0xffffffffu, kbase + kBlockN > lim || kbase < lo || notes != 0)) {
+#pragma unroll
+                for (int i = 0; i < kBlockN; ++i)
+                    if (kbase + i >= lim || kbase + i < lo || ((notes >> (i / 16)) & 1u)) s[i] = -INFINITY;
+            }
+            const float mx = fmaxf(fmaxf(chunk_max32(s, 0), chunk_max32(s, 32)), fmaxf(chunk_max32(s, 64), chunk_max32(s, 96)));
+            float m_prev = -INFINITY;
+            if (j > 0) {
+                good = wait_tagged_max(mref_w + 8u * (uint32_t)((g ^ 1) * kBlockM + r), (uint32_t)(j - 1), m_prev, abort_flag, p.wait_limit);
+                if (!__all_sync(0xffffffffu, good)) {
+                    ok = false;
+                    break;
+                }
+            }
+            const float t_max = mx * c;
+            const float m_cur = (t_max > m_prev + kRescaleThreshold) ? t_max : m_prev;
+            if (j + 1 < n_kv)
+                st_relaxed_shared_u64(mref_w + 8u * (uint32_t)(g * kBlockM + r), ((unsigned long long)(uint32_t)j << 32) | __float_as_uint(m_cur));
+            if (m_cur != m_seen) {
+                lu *= ex2_approx(m_seen - m_cur);
+                m_seen = m_cur;
+            }
+            const float mu = (m_cur == -INFINITY) ? 0.f : m_cur;
+            const int pb = j % F::kPBufs;
+            if (j >= F::kPBufs) {
+                good = wait_bounded(bar_pv_done(pb), (uint32_t)(((j - F::kPBufs) / F::kPBufs) & 1), abort_flag, p.wait_limit);
+                if (!__all_sync(0xffffffffu, good)) {
+                    ok = false;
+                    break;
+                }
+            }
+            // (all on MUFU: the polynomial of the dense forward would lose a NaN)
+            float2 lu2 = make_float2(0.f, 0.f);
+            const uint32_t taddr_p = tmem + lane_off + F::col_p(pb);
+            exp_store_half<0, 0>(s, c, mu, taddr_p, lu2);
+            exp_store_half<0, 1>(s, c, mu, taddr_p, lu2);
+            lu += lu2.x + lu2.y;
+            const float alpha = (m_cur != m_prev) ? ex2_approx(m_prev - m_cur) : 1.f;
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                good = wait_bounded(bar_pv_done((j - 1) % F::kPBufs), (uint32_t)(((j - 1) / F::kPBufs) & 1), abort_flag, p.wait_limit);
+                if (!__all_sync(0xffffffffu, good)) {
+                    tmem_wait_st();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int q4 = 0; q4 < D / 32 + 1; ++q4) {   // O and its row-sum columns
+                    const uint32_t ocol = tmem + lane_off + F::kColO + 32u * q4;
+                    uint32_t u[32];
+                    tmem_ld32(ocol, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        reg_after_wait(u[i]);
+                        u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+                    }
+                    tmem_st32(ocol, u);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p_full(pb));
+        }
+
+        // ---------------------------------------------------------- epilogue
+        const bool have_o = n_kv > 0;
+        bool good = ok;
+        if (good && have_o) {
+            good = __all_sync(0xffffffffu, wait_bounded(bar_drain, 0, abort_flag, p.wait_limit));
+            if (good) tc_fence_after();
+        }
+        epi[g * kBlockM + r] = m_seen;
+        epi[(2 + g) * kBlockM + r] = lu;
+        epi[(4 + g) * kBlockM + r] = __uint_as_float(nan_groups);
+        good = !named_bar_or(kBarQuadBase + qd, 64, !good);
+        const float m0w = epi[r], m1w = epi[kBlockM + r];
+        const float m_fin = fmaxf(m0w, m1w);
+        const float f0 = (m0w == m_fin) ? 1.f : ex2_approx(m0w - m_fin);
+        const float f1 = (m1w == m_fin) ? 1.f : ex2_approx(m1w - m_fin);
+        const float lu_row = epi[2 * kBlockM + r] * f0 + epi[3 * kBlockM + r] * f1;
+        nan_groups = __float_as_uint(epi[4 * kBlockM + r]) | __float_as_uint(epi[5 * kBlockM + r]);
+        if (good) {
+            float l_row = 0.f;
+            if (have_o) {
+                uint32_t u[32];
+                tmem_ld32(tmem + lane_off + F::kColL, u);
+                tmem_wait_ld();
+                reg_after_wait(u[0]);
+                l_row = __uint_as_float(u[0]);
+            }
+            const float inv_row = l_row == 0.f ? 0.f : 1.f / l_row;
+#pragma unroll
+            for (int q4 = 0; q4 < D / 64; ++q4) {
+                const int col0 = g * (D / 2) + 32 * q4;
+                const float inv_l = ((nan_groups >> (col0 / kGroup)) & 1u) ? __int_as_float(0x7fc00000) : inv_row;
+                uint32_t u[32];
+                if (have_o) {
+                    tmem_ld32(tmem + lane_off + F::kColO + (uint32_t)col0, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) reg_after_wait(u[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] = 0u;
+                }
+                auto two = [&](int a, int z) { return pack_bf16x2(__uint_as_float(u[a]) * inv_l, __uint_as_float(u[z]) * inv_l); };
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    // columns (0,4) (1,5) (2,6) (3,7) of 8 channels, back in order
+                    const int cc = col0 / 8 + v4, u0 = 8 * v4;
+                    sts16(q_tile + (uint32_t)((cc >> 3) * kSwizzleBoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)),
+                          two(u0, u0 + 2), two(u0 + 4, u0 + 6), two(u0 + 1, u0 + 3), two(u0 + 5, u0 + 7));
+                }
+            }
+            if (g == 0 && row < p.rows.R)
+                p.lse[((size_t)b * p.H_kv + h) * (size_t)p.rows.R + row] =
+                    lu_row == 0.f ? -INFINITY : (m_fin + log2f(lu_row)) * 0.69314718055994531f;
+        }
+        fence_proxy_async_smem();
+        const bool any_bad = named_bar_or(kBarSoftmaxAll, kSoftmaxWarps * 32, !good);
+        if (!any_bad && threadIdx.x == 0) {
+            for (int bx = 0; bx < F::kOBoxes; ++bx) tma_store_4d(&tm_o, q_tile + bx * kSwizzleBoxBytes, bx * 64, m0, h, b);
+            bulk_commit_group();
+            bulk_wait_group_read0();
+        }
+        tc_fence_before();
+    }
+
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace kv4
+}  // namespace fa

@@ -330,6 +330,12 @@ ATTEND = [
     (1, 1, 1, 1, 128, 256, 16, [4096], None, False, -1),              # one head over many CTAs
     (1, 1, 1, 3, 64, 4096, 1, [4001], None, True, 3000),              # one page, window over many CTAs
     (40, 2, 2, 1, 64, 16, 4, list(range(1, 41)), None, False, -1),    # many short sequences
+    (1, 1, 1, 128, 128, 32, 4, [128], None, True, -1),                # a whole prompt: one block of rows
+    (2, 2, 2, 129, 64, 64, 8, [129, 500], None, True, -1),            # a second block of one row
+    (2, 8, 2, 70, 128, 48, 10, [470, 60], [70, 33], True, 100),       # blocks that span heads; window; ragged
+    (1, 3, 1, 64, 128, 128, 3, [301], None, False, -1),               # no causal mask
+    (1, 6, 2, 300, 64, 32, 40, [1111], None, True, 500),
+    (3, 4, 4, 200, 128, 16, 13, [200, 0, 7], [200, 0, 200], True, -1),
 ]
 
 
@@ -345,36 +351,39 @@ def test_attention_matches_the_oracle(B, H, H_kv, N, d, page, maxp, key_lens, q_
 
 @pytest.mark.parametrize("sigma,scale", [(4.0, 0.5), (0.05, 1.0), (1.0, 30.0), (2.0 ** -60, 1.0)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_attention_on_steep_and_flat_scores(sigma, scale, d):
+@pytest.mark.parametrize("N", [2, 50])
+def test_attention_on_steep_and_flat_scores(sigma, scale, d, N):
     # steep: scores up to thousands, one key takes all; flat: every key counts alike
     key_lens = [700, 333]
     c = filled(2, 1, 16, d, 44, key_lens, 31, sigma=sigma)
-    bits = normal_bf16((2, 3, 2, d), 32, 0, min(sigma, 4.0))
+    bits = normal_bf16((2, 3, N, d), 32, 0, min(sigma, 4.0))
     o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, None, scale, True, -1)
     assert guards
     check(c, bits, key_lens, None, scale, True, -1, o, lse, what=f"sigma {sigma}")
 
 
-def test_scores_that_grow_along_the_keys():
+@pytest.mark.parametrize("N", [1, 20])
+def test_scores_that_grow_along_the_keys(N):
     # every tile moves the reference max: all the rescaling there is
     def edit(k, v):
         ramp = np.linspace(0.0, 6.0, k.shape[2])[None, None, :, None]
         k[:] = f32_to_bf16_bits((0.01 * bf16_bits_to_f32(k) + ramp).astype(np.float32))
     c = filled(1, 2, 16, 128, 60, [960], 33, edit=edit)
-    bits = f32_to_bf16_bits(np.ones((1, 4, 1, 128), np.float32))
+    bits = f32_to_bf16_bits(np.ones((1, 4, N, 128), np.float32))
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [960], None, 0.5, False, -1)
     check(c, bits, [960], None, 0.5, False, -1, o, lse)
 
 
-@pytest.mark.parametrize("N,rows", [(3, 3), (12, 24)])
-def test_what_a_query_does_not_see_has_no_influence(N, rows):
+@pytest.mark.parametrize("N,rows", [(3, 3), (12, 24), (40, 80), (150, 300)])
+@pytest.mark.parametrize("page", [16, 32])
+def test_what_a_query_does_not_see_has_no_influence(N, rows, page):
     # keys and values of the last tokens are NaN or infinite: the queries before them stay clean,
     # those that see them do not
     def edit(k, v):
         k[0, :, -2, 5] = 0x7FC0
         v[0, :, -1, 70] = 0x7F80
     key_lens = [200]
-    c = filled(1, 1, 16, 128, 13, key_lens, 34, edit=edit)
+    c = filled(1, 1, page, 128, 13, key_lens, 34, edit=edit)
     bits = normal_bf16((1, rows // N, N, 128), 35, 0)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, -1)
     check(c, bits, key_lens, None, 0.09, True, -1, o, lse)
@@ -383,15 +392,16 @@ def test_what_a_query_does_not_see_has_no_influence(N, rows):
     # behind a window too: an early poisoned value is out of sight of the last query
     def edit2(k, v):
         v[0, :, 190, 3] = 0xFF80
-    c = filled(1, 1, 16, 128, 13, key_lens, 34, edit=edit2)
+    c = filled(1, 1, page, 128, 13, key_lens, 34, edit=edit2)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, 8)
     check(c, bits, key_lens, None, 0.09, True, 8, o, lse)
 
 
-def test_bad_pages_are_masked():
+@pytest.mark.parametrize("N", [3, 30])
+def test_bad_pages_are_masked(N):
     table = [[0, -1, 5, 2, 99, 1]]
     c = filled(1, 2, 16, 64, 6, [90], 36, table=table)
-    bits = normal_bf16((1, 4, 3, 64), 37, 0)
+    bits = normal_bf16((1, 4, N, 64), 37, 0)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [90], None, 0.125, True, -1)
     check(c, bits, [90], None, 0.125, True, -1, o, lse)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [5000], [2], 0.125, True, -1)     # length clamped to the pages
@@ -464,11 +474,12 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(lse.cpu().numpy()[0, h] - rl) <= el)
 
 
-def test_results_are_the_same_bits_each_time_and_on_another_stream():
+@pytest.mark.parametrize("N", [1, 5, 40])
+def test_results_are_the_same_bits_each_time_and_on_another_stream(N):
     import torch
     key_lens = [1900, 5, 777]
     c = filled(3, 2, 16, 128, 120, key_lens, 51)
-    q = to_device_bf16(normal_bf16((3, 8, 2, 128), 52, 0))
+    q = to_device_bf16(normal_bf16((3, 8, N, 128), 52, 0))
     o, lse, _ = run_kv4(c, q, key_lens, None, 0.09, True, -1)
     side = torch.cuda.Stream()
     for stream in (None, side, side.cuda_stream):
@@ -511,10 +522,10 @@ def test_captured_calls_replay_and_graphs_share_a_workspace():
     c.append(k, v, [1500, 1500])
     lens = ints([900, 1400])
     (k1, v1), _ = tokens(B, H_kv, 1, d, 72)
-    n = max(fa_fwd_kv4_workspace_size(B, H, H_kv, N, d) for N in (1, 5))
+    n = max(fa_fwd_kv4_workspace_size(B, H, H_kv, N, d) for N in (1, 5, 33))
     ws = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
     graphs = []
-    for N in (1, 5):
+    for N in (1, 5, 33):
         bits = normal_bf16((B, H, N, d), 73, 0)
         q = to_device_bf16(bits)
         o, lse = torch.empty_like(q), torch.empty((B, H, N), dtype=torch.float32, device="cuda")
