@@ -49,7 +49,14 @@ struct RowsCfg {
     // groups), then its 32 keys' NaN bits per group
     static constexpr int kNoteBytes = kMakers * 4 * (1 + D / kGroup);
     static constexpr int kNoteOff = kEpiOff + 3 * kGroups * kBlockM * 4;
-    static constexpr int kSmemBytes = kNoteOff + kNotes * kNoteBytes + 1024;
+    // staging of the codes: per maker warp, pass and lane 16 bytes of K, 16 of V, 4 of scales of each
+    static constexpr int kPass = D / kGroup;
+    static constexpr int kStageOff = (kNoteOff + kNotes * kNoteBytes + 15) / 16 * 16;
+    static constexpr int kStageV = kPass * 32 * 16;
+    static constexpr int kStageKS = 2 * kStageV;
+    static constexpr int kStageVS = kStageKS + kPass * 32 * 4;
+    static constexpr int kStageWarp = kStageVS + kPass * 32 * 4;
+    static constexpr int kSmemBytes = kStageOff + kMakers * kStageWarp + 1024;
     static_assert(kSmemBytes <= 232448 && kSmemBytes > 116 * 1024, "one CTA per SM");
 };
 
@@ -60,6 +67,19 @@ __device__ __forceinline__ uint4 code_order(uint4 x) {
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int D, bool kOneRun>
@@ -142,71 +162,71 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
         // Warp w makes keys 32w .. 32w + 31 of each tile.  A lane takes one group of 32 channels
         // (a scale, 16 bytes of codes) of a key: 8 (d = 128) or 16 keys of the same group lie in
         // neighbouring lanes, which store to different banks.
-        constexpr int kG = D / kGroup, kKeys = 32 / kG, kPass = 32 / kKeys;
+        // The codes come through shared memory by cp.async, one tile ahead, each lane its own
+        // bytes: a load to a register would have to land at every proxy fence.
+        constexpr int kG = D / kGroup, kKeys = 32 / kG, kPass = C::kPass;
+        static_assert(kPass * kKeys == 32, "a warp's keys");
         constexpr int kRuns = kOneRun ? 1 : 2;
         const int w = warp - kMakerWarp;
         const int key_l = lane % kKeys, grp = lane / kKeys;
+        const uint32_t stage = base + (uint32_t)(C::kStageOff + w * C::kStageWarp);
         bool ok = true;
-        int page[kRuns], off[kRuns];
-        auto look_up = [&](int j) {
+        // first rows of the warp's runs of tiles j0 .. j0 + 31, a tile per lane (~0: not there)
+        uint32_t l_row[kRuns], row[kRuns];
+        auto rows_of = [&](int j) {
+            if ((j & 31) == 0) {
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i) {
-                const int pos = x.lo + j * kBlockN + w * 32 + 16 * i;
-                page[i] = -1;
-                off[i] = 0;
-                if (j < n_kv && pos < x.hi) page[i] = page_of(p.pg, b, page_div(p.pg, pos, off[i]));
+                for (int i = 0; i < kRuns; ++i) {
+                    const int pos = x.lo + (j + lane) * kBlockN + w * 32 + 16 * i;
+                    l_row[i] = 0xffffffffu;
+                    if (j + lane < n_kv && pos < x.hi) {
+                        int off;
+                        const int page = page_of(p.pg, b, page_div(p.pg, pos, off));
+                        if (page >= 0)
+                            l_row[i] = ((uint32_t)page * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size + (uint32_t)off;
+                    }
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) row[i] = __shfl_sync(0xffffffffu, l_row[i], j & 31);
         };
-        uint4 kc[kPass], vc[kPass];
-        uint32_t sc[kPass];          // K's scale in the low half, V's in the high one
-        uint32_t vrow[kPass];        // V's row, ~0 where there is none
-        uint32_t gone = 0;           // runs of the loaded tile that are not there
-        // Tile j's K and all its scales; load_v then takes its V.  Each is on its way while
-        // the other tensor's tile is made.
-        auto load_k = [&](int j) {
-            gone = 0;
+        auto copy_k = [&]() {            // K and both scales of the rows just looked up
 #pragma unroll
             for (int o = 0; o < kPass; ++o) {
                 const int i = o * kKeys / 16 % kRuns, in = o * kKeys - (kOneRun ? 0 : i * 16);
-                kc[o] = make_uint4(0, 0, 0, 0);
-                sc[o] = 0;
-                vrow[o] = 0xffffffffu;
-                if (page[i] >= 0) {
-                    const uint32_t row = ((uint32_t)page[i] * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size +
-                                         (uint32_t)(off[i] + in + key_l);
-                    kc[o] = __ldg(reinterpret_cast<const uint4*>(p.k_codes + (size_t)row * (D / 2)) + grp);
-                    sc[o] = __ldg(p.k_scales + (size_t)row * kG + grp);
-                    vrow[o] = row;
-                    // rows behind the last key may hold anything: their V counts as zero
-                    if (x.lo + j * kBlockN + w * 32 + o * kKeys + key_l < x.kl)
-                        sc[o] |= (uint32_t)__ldg(p.v_scales + (size_t)row * kG + grp) << 16;
-                } else {
-                    gone |= kOneRun ? 3u : 1u << i;
+                if (row[i] != 0xffffffffu) {
+                    const size_t r = row[i] + (uint32_t)(in + key_l);
+                    cp_async<16>(stage + (uint32_t)((o * 32 + lane) * 16), p.k_codes + r * (D / 2) + grp * 16);
+                    cp_async<4>(stage + (uint32_t)(C::kStageKS + (o * 32 + lane) * 4), p.k_scales + r * kG + (grp & ~1));
+                    cp_async<4>(stage + (uint32_t)(C::kStageVS + (o * 32 + lane) * 4), p.v_scales + r * kG + (grp & ~1));
                 }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_v = [&]() {
+        auto copy_v = [&](const uint32_t (&vr)[kRuns]) {
 #pragma unroll
             for (int o = 0; o < kPass; ++o) {
-                vc[o] = make_uint4(0, 0, 0, 0);
-                if (vrow[o] != 0xffffffffu) vc[o] = __ldg(reinterpret_cast<const uint4*>(p.v_codes + (size_t)vrow[o] * (D / 2)) + grp);
+                const int i = o * kKeys / 16 % kRuns, in = o * kKeys - (kOneRun ? 0 : i * 16);
+                if (vr[i] != 0xffffffffu)
+                    cp_async<16>(stage + (uint32_t)(C::kStageV + (o * 32 + lane) * 16),
+                                 p.v_codes + (size_t)(vr[i] + (uint32_t)(in + key_l)) * (D / 2) + grp * 16);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto store = [&](uint32_t slot, int o, const uint4& c, uint32_t s) {
             const uint32_t s2 = __byte_perm(s, s, 0x1010), z2 = minus_24(s2);
             const int key = w * 32 + o * kKeys + key_l;
             const uint32_t at = slot + (uint32_t)((grp >> 1) * F::kBoxBytes + key * 128);
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sts16(at + (uint32_t)(((((grp & 1) << 2) + i) ^ (key & 7)) << 4), codes_to_bf16x2(0, cw[i], s2, z2),
-                      codes_to_bf16x2(1, cw[i], s2, z2), codes_to_bf16x2(2, cw[i], s2, z2), codes_to_bf16x2(3, cw[i], s2, z2));
+                sts16(at + (uint32_t)(((((grp & 1) << 2) + i) ^ (key & 7)) << 4), codes_to_bf16x2(0, word[i], s2, z2),
+                      codes_to_bf16x2(1, word[i], s2, z2), codes_to_bf16x2(2, word[i], s2, z2), codes_to_bf16x2(3, word[i], s2, z2));
         };
         if (n_kv > 0) {
-            look_up(0);
-            load_k(0);
-            load_v();
-            look_up(1);
+            rows_of(0);
+            copy_k();
+            copy_v(row);
             // Q into the order of the codes: row 32w + lane
             ok = __all_sync(0xffffffffu, wait_bounded(bar_q_full, 0, abort_flag, p.wait_limit));
             if (ok) {
@@ -214,9 +234,7 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
 #pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
                     const uint32_t a = row + (uint32_t)((i >> 3) * F::kBoxBytes + (((i & 7) ^ (lane & 7)) << 4));
-                    uint4 v;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-                    v = code_order(v);
+                    const uint4 v = code_order(lds16(a));
                     sts16(a, v.x, v.y, v.z, v.w);
                 }
                 fence_proxy_async_smem();
@@ -226,6 +244,36 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
         }
         for (int j = 0; j < n_kv && ok; ++j) {
             const int sk = j % F::kStagesK, sv = j % F::kStagesV;
+            uint32_t here[kRuns];        // of this tile; row moves on to the next one
+            uint32_t gone = 0;           // runs that are not there
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                here[i] = row[i];
+                if (here[i] == 0xffffffffu) gone |= kOneRun ? 3u : 1u << i;
+            }
+            uint4 cw[kPass];
+            uint32_t sc[kPass];          // K's scale in the low half, V's in the high one
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) {
+                const int i = o * kKeys / 16 % kRuns;
+                cw[o] = make_uint4(0, 0, 0, 0);
+                sc[o] = 0;
+                if (here[i] != 0xffffffffu) {
+                    cw[o] = lds16(stage + (uint32_t)((o * 32 + lane) * 16));
+                    uint32_t ks, vs;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ks) : "r"(stage + (uint32_t)(C::kStageKS + (o * 32 + lane) * 4)));
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(stage + (uint32_t)(C::kStageVS + (o * 32 + lane) * 4)));
+                    // rows behind the last key may hold anything: their V counts as zero
+                    if (x.lo + j * kBlockN + w * 32 + o * kKeys + key_l >= x.kl) vs = 0;
+                    sc[o] = __byte_perm(ks, vs, (grp & 1) ? 0x7632 : 0x5410);
+                }
+            }
+            if (j + 1 < n_kv) rows_of(j + 1);
+            else
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) row[i] = 0xffffffffu;
+            copy_k();
             ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(0, sk), ((uint32_t)(j / F::kStagesK) & 1u) ^ 1u, abort_flag, p.wait_limit));
             if (!ok) break;
             // notes first: whoever sees this tile's scores sees them too
@@ -245,24 +293,26 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
             }
             if (lane == 0) note(j)[w] = gone | (any_bad ? 4u : 0u);
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sk), o, kc[o], sc[o]);
+            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sk), o, cw[o], sc[o]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_full(0, sk));
-            uint32_t sv2[kPass];
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) sv2[o] = sc[o] >> 16;
-            load_k(j + 1);
-            look_up(j + 2);
+            for (int o = 0; o < kPass; ++o) {
+                cw[o] = make_uint4(0, 0, 0, 0);
+                if (here[o * kKeys / 16 % kRuns] != 0xffffffffu) cw[o] = lds16(stage + (uint32_t)(C::kStageV + (o * 32 + lane) * 16));
+            }
+            copy_v(row);
             ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(1, sv), ((uint32_t)(j / F::kStagesV) & 1u) ^ 1u, abort_flag, p.wait_limit));
             if (!ok) break;
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sv), o, vc[o], sv2[o]);
+            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sv), o, cw[o], sc[o] >> 16);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_full(1, sv));
-            load_v();
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");   // nothing lands after the CTA's end
         __syncwarp();
     } else if (warp >= kProducerWarp) {
         setmaxnreg_dec<kRegsRowsControl>();
