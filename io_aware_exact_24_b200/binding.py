@@ -24,6 +24,7 @@ FA_ERR_DEVICE_TIMEOUT = -6
 _LIB_NAME = "libfa_b200.so"
 _lock = threading.Lock()
 _lib = None
+_fast = None   # the marshalling module of the 4-bit cache entry points, once the library is loaded
 
 
 class FaError(RuntimeError):
@@ -42,7 +43,7 @@ def library_path() -> str:
 
 def load_library() -> ctypes.CDLL:
     """Load the compiled library (raises if it has not been built)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -116,6 +117,13 @@ def load_library() -> ctypes.CDLL:
             lib.fa_last_error.restype = ctypes.c_char_p
             lib.fa_version.argtypes = []
             lib.fa_version.restype = i32
+            try:
+                from . import _fastcall
+            except ImportError as e:
+                raise ImportError("the _fastcall module is missing: build it with `python -m io_aware_exact_24_b200.build`") from e
+            _fastcall.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)))
+            _fast = _fastcall
             _lib = lib
     return _lib
 
@@ -287,14 +295,18 @@ def fa_fwd_splitkv_noalloc(q, k, v, o, lse, B, H, N_q, N_k, d, scale, causal, ke
     return st
 
 
+def _marshaller():
+    if _fast is None:
+        load_library()
+    return _fast
+
+
 def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, new_lens, B,
                   H_kv, N_new, d, num_pages, page_size, max_pages, stream=None, check=True) -> int:
     """``fa_kv4_append`` of include/fa.h: quantise new tokens into the 4-bit paged cache."""
-    st = load_library().fa_kv4_append(_addr(k), _addr(v), _addr(k_codes), _addr(k_scales),
-                                      _addr(v_codes), _addr(v_scales), _addr(block_table),
-                                      _addr(key_lens), _addr(new_lens), int(B), int(H_kv),
-                                      int(N_new), int(d), int(num_pages), int(page_size),
-                                      int(max_pages), _stream(stream))
+    st = (_fast or _marshaller()).fa_kv4_append(
+        k, v, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, new_lens, B, H_kv, N_new,
+        d, num_pages, page_size, max_pages, _stream(stream))
     if check and st != FA_OK:
         raise FaError(st, "fa_kv4_append")
     return st
@@ -303,11 +315,9 @@ def fa_kv4_append(k, v, k_codes, k_scales, v_codes, v_scales, block_table, key_l
 def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, first, k, v, B, H_kv,
                 N, d, num_pages, page_size, max_pages, stream=None, check=True) -> int:
     """``fa_kv4_read`` of include/fa.h: a span of the 4-bit cache as dense bf16."""
-    st = load_library().fa_kv4_read(_addr(k_codes), _addr(k_scales), _addr(v_codes),
-                                    _addr(v_scales), _addr(block_table), _addr(key_lens),
-                                    _addr(first), _addr(k), _addr(v), int(B), int(H_kv), int(N),
-                                    int(d), int(num_pages), int(page_size), int(max_pages),
-                                    _stream(stream))
+    st = (_fast or _marshaller()).fa_kv4_read(
+        k_codes, k_scales, v_codes, v_scales, block_table, key_lens, first, k, v, B, H_kv, N, d,
+        num_pages, page_size, max_pages, _stream(stream))
     if check and st != FA_OK:
         raise FaError(st, "fa_kv4_read")
     return st
@@ -322,13 +332,10 @@ def fa_fwd_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q
                H, H_kv, N_q, d, num_pages, page_size, max_pages, scale, causal, window_left,
                workspace, workspace_bytes, stream=None, check=True) -> int:
     """``fa_fwd_kv4`` of include/fa.h: attention over the 4-bit paged cache."""
-    st = load_library().fa_fwd_kv4(_addr(q), _addr(k_codes), _addr(k_scales), _addr(v_codes),
-                                   _addr(v_scales), _addr(block_table), _addr(key_lens),
-                                   _addr(q_lens), _addr(o), _addr(lse), int(B), int(H), int(H_kv),
-                                   int(N_q), int(d), int(num_pages), int(page_size),
-                                   int(max_pages), float(scale), int(bool(causal)),
-                                   int(window_left), _addr(workspace), int(workspace_bytes),
-                                   _stream(stream))
+    st = (_fast or _marshaller()).fa_fwd_kv4(
+        q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o, lse, B, H, H_kv,
+        N_q, d, num_pages, page_size, max_pages, scale, causal, window_left, workspace,
+        workspace_bytes, _stream(stream))
     if check and st != FA_OK:
         raise FaError(st, "fa_fwd_kv4")
     return st

@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +22,11 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", 
               "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
 
+# CPython module that marshals the calls of a decoding step (see csrc/fa_fastcall.c)
+FAST_SRC = os.path.join(CSRC, "fa_fastcall.c")
+FAST_OUT = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -28,7 +34,19 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def build_fastcall(force: bool = False) -> str:
+    """The marshalling module, for this interpreter."""
+    if not force and os.path.exists(FAST_OUT) and os.path.getmtime(FAST_SRC) <= os.path.getmtime(FAST_OUT):
+        return FAST_OUT
+    tmp = FAST_OUT + f".tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                    "-o", tmp, FAST_SRC], check=True)
+    os.replace(tmp, FAST_OUT)
+    return FAST_OUT
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_fastcall(force)
     if not force and os.path.exists(OUT):
         t = os.path.getmtime(OUT)
         if all(os.path.getmtime(f) <= t for f in DEPENDS):

@@ -14,9 +14,6 @@
 #include "fa_kv4_attend.cuh"
 #include "fa_kv4_kernel.cuh"
 
-#ifndef FA_ROWS_MIN
-#define FA_ROWS_MIN 33
-#endif
 namespace {
 
 using fa_internal::cuda_fail;
@@ -86,6 +83,15 @@ unsigned long long next_ticket() {
 // Rows per block: one MMA column block holds 8 query rows.
 int row_block(long long R) { return R <= 8 ? 8 : 16; }
 int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
+
+// Whether the kernel for many rows (fa_kv4_rows.cuh) is the quicker one.  Per 128 keys it takes
+// about 1.6 us for each wave of its CTAs (128 rows each, one CTA per SM); the kernel for few rows
+// takes 0.84 us of an SM for 16 rows, spread evenly.  Measured on both sides: 8 heads, 8192 keys,
+// 512 rows 103 and 95 us; 64 heads, 4096 keys, 64 rows 57 and 58 us, 128 rows 57 and 101 us.
+bool many_rows(long long R, long long heads, int num_sms) {
+    const long long waves = ((R + 127) / 128 * heads + num_sms - 1) / num_sms;
+    return R > 16 && 84 * ((R + 15) / 16) * heads > 160 * waves * num_sms;
+}
 
 // Workspace of the attention: two partial results per CTA, then the arrival words.
 struct Layout {
@@ -250,7 +256,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     rows.window = window_left < 0 ? -1 : window_left;
     const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (R >= FA_ROWS_MIN) {
+    if (many_rows(R, (long long)B * H_kv, sms)) {
         kv4::RowsParams p{};
         p.k_codes = static_cast<const uint8_t*>(k_codes);
         p.k_scales = static_cast<const uint16_t*>(k_scales);

@@ -688,26 +688,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                 // the first CTA have it first
                 const long long first = (long long)(2 * cf + (share(cf) >= item_first ? 0 : 1)) * RB;
                 auto at = [&](int c) { return c == cf ? first : (long long)(2 * c) * RB; };
-                // sums, 4 channels a thread; with few rows several threads share the CTAs of one.
-                // The first of them are on their way while the rows' statistics are made.
+                // sums, 4 channels a thread: of up to kEach rows, or, with few rows, of some of the
+                // CTAs of one row.  kAhead * kEach loads at a time, the first of them on their way
+                // while the rows' statistics are made.
                 const int items = nr * (D / 4);
                 const int groups = items * 2 > kThreads ? 1 : kThreads / items;
-                constexpr int kAhead = 4;
-                float mc[kAhead];
-                float4 y[kAhead];
-                const int gi = groups == 1 ? 0 : tid / items;
-                const int rr0 = (tid - gi * items) / (D / 4), c40 = tid % (D / 4);
-                const bool in = gi < groups && rr0 < nr;
+                constexpr int kEach = RB * (D / 4) / kThreads, kAhead = NB == 1 ? 2 : 4;
+                static_assert(kEach * kThreads == RB * (D / 4), "rows of a block");
+                float mc[kAhead][kEach];
+                float4 y[kAhead][kEach];
+                const bool one = groups == 1;    // one thread has all CTAs of a row
+                const int gi = one ? 0 : tid / items, step = one ? kAhead : kAhead * kEach * groups;
+                const int it0 = tid - gi * items, c40 = tid % (D / 4);
+                auto row_of = [&](int e) { return one ? (it0 + e * kThreads) / (D / 4) : it0 / (D / 4); };
+                auto fetch = [&](int c0) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const int c = cf + gi + i * groups;
-                    mc[i] = -INFINITY;
-                    y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (in && c <= cl) {
-                        mc[i] = __ldcg(p.part_ml + (at(c) + rr0) * 4);
-                        y[i] = __ldcg(reinterpret_cast<const float4*>(p.part + (at(c) + rr0) * D) + c40);
-                    }
-                }
+                    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            // (without branches, so that the loads go out together)
+                            const int c = one ? c0 + i : c0 + (i * kEach + e) * groups;
+                            const long long r = at(min(c, cl)) + min(row_of(e), nr - 1);
+                            mc[i][e] = __ldcg(p.part_ml + r * 4);
+                            y[i][e] = __ldcg(reinterpret_cast<const float4*>(p.part + r * D) + c40);
+                            if (c > cl) mc[i][e] = -INFINITY;
+                        }
+                };
+                fetch(cf + gi);
                 // statistics of each row: a warp per row, a lane per CTA
                 float* const fin = st_max;       // [RB] merged max, [RB] 1 / merged sum (the warps' own are used up)
                 for (int rr = warp; rr < nr; rr += kWarps) {
@@ -739,13 +746,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     }
                 }
                 __syncthreads();
-                auto add = [](float4& a, float m, float ref, const float4& v) {
-                    const float f = m == -INFINITY ? 0.f : ex2_approx(m - ref);
-                    a.x = fmaf(v.x, f, a.x);
-                    a.y = fmaf(v.y, f, a.y);
-                    a.z = fmaf(v.z, f, a.z);
-                    a.w = fmaf(v.w, f, a.w);
-                };
                 auto put = [&](int rr, int c4, const float4& a) {
                     const float inv = fin[RB + rr];
                     uint2 pk;
@@ -753,36 +753,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     pk.y = pack_bf16x2(a.z * inv, a.w * inv);
                     *reinterpret_cast<uint2*>(p.o + (row0 + rr) * D + 4 * c4) = pk;
                 };
-                auto rest = [&](float4& a, int c, int rr, int c4) {
-                    const float m = fin[rr];
-#pragma unroll 8
-                    for (; c <= cl; c += groups)
-                        add(a, __ldcg(p.part_ml + (at(c) + rr) * 4), m,
-                            __ldcg(reinterpret_cast<const float4*>(p.part + (at(c) + rr) * D) + c4));
-                };
-                float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (in) {
+                float4 a[kEach];
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) add(a0, mc[i], fin[rr0], y[i]);
-                    rest(a0, cf + gi + kAhead * groups, rr0, c40);
-                }
-                if (groups == 1) {
-                    if (in) put(rr0, c40, a0);
-                    for (int it = tid + kThreads; it < items; it += kThreads) {
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                        rest(a, cf, it / (D / 4), it % (D / 4));
-                        put(it / (D / 4), it % (D / 4), a);
+                for (int e = 0; e < kEach; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = cf + gi; c <= cl;) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const float m = fin[min(row_of(e), RB - 1)];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const float f = mc[i][e] == -INFINITY ? 0.f : ex2_approx(mc[i][e] - m);
+                            a[e].x = fmaf(y[i][e].x, f, a[e].x);
+                            a[e].y = fmaf(y[i][e].y, f, a[e].y);
+                            a[e].z = fmaf(y[i][e].z, f, a[e].z);
+                            a[e].w = fmaf(y[i][e].w, f, a[e].w);
+                        }
                     }
+                    c += step;
+                    if (c <= cl) fetch(c);
+                }
+                if (!one) {
+#pragma unroll
+                    for (int e = 1; e < kEach; ++e)
+                        a[0].x += a[e].x, a[0].y += a[e].y, a[0].z += a[e].z, a[0].w += a[e].w;
+                }
+                if (one) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (it0 + e * kThreads < items) put(row_of(e), c40, a[e]);
                 } else {
-                    if (in) *reinterpret_cast<float4*>(red + tid * 4) = a0;
+                    if (gi < groups) *reinterpret_cast<float4*>(red + tid * 4) = a[0];
                     __syncthreads();
                     if (tid < items) {
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                         for (int i = 0; i < groups; ++i) {
-                            const float4 v = *reinterpret_cast<const float4*>(red + (i * items + tid) * 4);
-                            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                            const float4 w = *reinterpret_cast<const float4*>(red + (i * items + tid) * 4);
+                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                         }
-                        put(rr0, c40, a);
+                        put(row_of(0), c40, v);
                     }
                 }
             }

@@ -24,7 +24,7 @@
 namespace fa {
 namespace kv4 {
 
-constexpr int kRowThreads512 = 512;          // 8 softmax warps, 4 control warps, 4 that make K and V tiles
+constexpr int kRowsThreads = 512;          // 8 softmax warps, 4 control warps, 4 that make K and V tiles
 constexpr int kMakerWarp = 12;
 constexpr int kMakers = 4;
 // Registers per thread: 512 x 128 at launch; 2 x 128 x 184 + 128 x 48 + 128 x 96 are as many.
@@ -32,9 +32,10 @@ constexpr uint32_t kRegsRowsSoftmax = 184;
 constexpr uint32_t kRegsRowsControl = 48;
 constexpr uint32_t kRegsRowsMaker = 96;
 // Tiles whose notes are kept.  A maker writes tile j's when the scores of tile j - stages are
-// done, so those of tile j - stages - 1 have been read, and with them its notes.
+// done, so the softmax warps have taken those of j - stages - 1 and j - stages - 2 out, one
+// each, and are through with all tiles before.
 constexpr int kNotes = 8;
-static_assert(kNotes > fa::Cfg<64>::kStagesK && kNotes > fa::Cfg<128>::kStagesK, "notes still to be read");
+static_assert(kNotes >= fa::Cfg<64>::kStagesK + 3 && kNotes >= fa::Cfg<128>::kStagesK + 3, "notes still to be read");
 
 template <int D>
 struct RowsCfg {
@@ -83,7 +84,7 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
 }
 
 template <int D, bool kOneRun>
-__global__ void __launch_bounds__(kRowThreads512, 1)
+__global__ void __launch_bounds__(kRowsThreads, 1)
     rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o, const RowsParams p) {
     using F = fa::Cfg<D>;
     using C = RowsCfg<D>;
@@ -140,14 +141,14 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_o);
     }
-    for (int i = threadIdx.x; i < kGroups * kBlockM; i += kRowThreads512) st_relaxed_shared_u64(mref_w + 8u * (uint32_t)i, ~0ull);
+    for (int i = threadIdx.x; i < kGroups * kBlockM; i += kRowsThreads) st_relaxed_shared_u64(mref_w + 8u * (uint32_t)i, ~0ull);
     if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(tmem_holder), kTmemCols);
         tmem_relinquish();
         tc_fence_before();
     }
     // the ones box of every V slot: the PV product's last columns sum the rounded P
-    for (int i = threadIdx.x; i < F::kStagesV * (F::kBoxBytes / 16); i += kRowThreads512) {
+    for (int i = threadIdx.x; i < F::kStagesV * (F::kBoxBytes / 16); i += kRowsThreads) {
         const uint32_t a = ring_slot(1, i / (F::kBoxBytes / 16)) + (uint32_t)F::kTileBytes + (uint32_t)(i % (F::kBoxBytes / 16)) * 16u;
         sts16(a, F::kOnesWord, F::kOnesWord, F::kOnesWord, F::kOnesWord);
     }
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
         const int row = m0 + r;
         int lo, lim;
         row_keys(p.rows, x.kl, x.ql, row, lo, lim);
+        if (row >= p.rows.R) lo = 0, lim = 0x7fffffff;   // no row: nothing of it is kept, and it asks for no mask
         const float c = p.scale_log2;
         float m_seen = -INFINITY, lu = 0.f;
         uint32_t nan_groups = 0;         // groups of V that a key this row sees holds as NaN
@@ -389,6 +391,22 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
             }
             tc_fence_after();
             const int kbase = x.lo + j * kBlockN;
+            float s[kBlockN];
+            {
+                uint32_t u[kBlockN];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+                    tmem_ld32(tmem + lane_off + F::col_s(0) + 32u * q4, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q4]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < kBlockN; ++i) {
+                    reg_after_wait(u[i]);
+                    s[i] = __uint_as_float(u[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_s_free);
             uint32_t notes = 0;          // bits 2w, 2w + 1: runs of warp w that are not there
             uint32_t any_nan = 0;
 #pragma unroll
@@ -408,22 +426,6 @@ __global__ void __launch_bounds__(kRowThreads512, 1)
                             }
                         }
             }
-            float s[kBlockN];
-            {
-                uint32_t u[kBlockN];
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4)
-                    tmem_ld32(tmem + lane_off + F::col_s(0) + 32u * q4, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q4]));
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < kBlockN; ++i) {
-                    reg_after_wait(u[i]);
-                    s[i] = __uint_as_float(u[i]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_s_free);
             if (__any_sync(0xffffffffu, kbase + kBlockN > lim || kbase < lo || notes != 0)) {
 #pragma unroll
                 for (int i = 0; i < kBlockN; ++i)

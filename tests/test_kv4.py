@@ -177,6 +177,27 @@ def test_without_a_gpu_valid_calls_report_no_device(lib):
         assert call(num_pages=0, kc=None, ks=None, vc=None, vs=None) == binding.FA_ERR_NO_DEVICE
 
 
+def test_arguments_become_the_same_call(lib):
+    """The marshalling module and ctypes hand the library the same values (B = 0: nothing is done)."""
+    import ctypes
+    import torch
+    t = torch.zeros(64, dtype=torch.uint8)
+    assert append(k=t, key_lens=None, B=0) == append(k=t.data_ptr(), key_lens=None, B=0) == binding.FA_OK
+    for kw in ({}, dict(d=96), dict(ws_bytes=16), dict(q=P + 2), dict(N=0), dict(scale=-1), dict(window=7, causal=1, H=0)):
+        a = dict(q=P, o=P, lse=P, kc=P, ks=P, vc=P, vs=P, table=P, key_lens=P, lens=P, B=1, H=2, H_kv=1, N=1, d=64,
+                 num_pages=4, page_size=16, max_pages=4, scale=0.125, causal=0, window=-1, ws=P, ws_bytes=1 << 40) | kw
+        if torch.cuda.is_available() and not kw:
+            continue
+        st = lib.fa_fwd_kv4(a["q"], a["kc"], a["ks"], a["vc"], a["vs"], a["table"], a["key_lens"], a["lens"], a["o"], a["lse"],
+                            a["B"], a["H"], a["H_kv"], a["N"], a["d"], a["num_pages"], a["page_size"], a["max_pages"],
+                            ctypes.c_float(a["scale"]), a["causal"], a["window"], a["ws"], a["ws_bytes"], None)
+        assert fwd(**kw) == st
+    for bad in (dict(q="x"), dict(B=1.5j), dict(B=1 << 40), dict(scale="y"), dict(ws_bytes=-1)):
+        with pytest.raises((TypeError, OverflowError)):
+            fwd(**bad)
+    assert fwd(B=np.int64(0), scale=np.float32(0.5)) == binding.FA_OK
+
+
 def test_workspace_size(lib):
     n = binding.fa_fwd_kv4_workspace_size(3, 8, 2, 1, 128)
     assert n > 0 and n % 256 == 0
