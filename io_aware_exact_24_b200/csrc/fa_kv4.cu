@@ -253,7 +253,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     rows.N_q = N_q;
     rows.R = (int)R;
     rows.causal = causal ? 1 : 0;
-    rows.window = window_left < 0 ? -1 : window_left;
+    rows.window = window_left < 0 ? -1 : std::min(window_left, kMaxPositions);
     const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (many_rows(R, (long long)B * H_kv, sms)) {

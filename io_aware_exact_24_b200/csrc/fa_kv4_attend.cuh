@@ -127,7 +127,10 @@ __device__ __forceinline__ unsigned long long arrive_claim(unsigned long long* w
 __device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long found, unsigned long long ticket,
                                             int n) {
     if (found != 0 && (found >> 16) != ticket) atomicCAS(word, found, ticket << 16);
-    const unsigned long long old = atomicAdd(word, 1ull);
+    // releases this CTA's partial results (all its threads', after their barrier) and, for the
+    // last one, acquires the others'
+    unsigned long long old;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
     if ((int)(old & 0xffffull) + 1 != n) return false;
     atomicExch(word, 0ull);
     return true;
@@ -167,16 +170,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     const int g = lane >> 2, t = lane & 3;       // MMA fragment coordinates
 
     // ------------------------------------------------ the line of units
-    {
+    Entry x;                         // of the current segment; first, of the thread's own entry
+    const bool few = p.E <= 32;      // then every warp makes the line by itself, an entry per lane
+    if (few) {
+        x = entry_of<RB>(p, min(lane, p.E - 1));
+        const int n = lane < p.E ? x.units * p.H_kv : 0;
+        int inc = n;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, sh);
+            if (lane >= sh) inc += y;
+        }
+        if (lane < p.E) pre[lane] = inc - n;     // (all warps the same)
+        if (lane == 31) pre[p.E] = inc;
+        __syncwarp();
+    } else {
         constexpr int kPer = kMaxEntries / kThreads;
+        const int per = (p.E + kThreads - 1) / kThreads;     // thread's entries: tid * per .. + per - 1
         int n[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            n[i] = 0;
-            if (i * kThreads < p.E) {            // thread's entries: tid * per .. + per - 1, per = ceil(E / kThreads)
-                const int per = (p.E + kThreads - 1) / kThreads, e = tid * per + i;
-                if (i < per && e < p.E) n[i] = entry_of<RB>(p, e).units * p.H_kv;
-            }
+            const int e = tid * per + i;
+            n[i] = i < per && e < p.E ? entry_of<RB>(p, e).units * p.H_kv : 0;
             sum += n[i];
         }
         int inc = sum;
@@ -189,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         __syncthreads();
         int at = inc - sum;
         for (int w = 0; w < warp; ++w) at += misc[w];
-        const int per = (p.E + kThreads - 1) / kThreads;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (i < per && tid * per + i < p.E) pre[tid * per + i] = at;
@@ -209,15 +223,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     // ------------------------------------------------ loading: a cursor ahead of the arithmetic
     int l_e, l_h, l_left;            // entry, head, units left in the item
     int l_units, l_lo, l_hi, l_b, l_pos;
-    {
+    if (few) {
+        l_e = __popc(__ballot_sync(0xffffffffu, lane < p.E && pre[min(lane, p.E)] <= u0)) - 1;
+        auto from = [&](int& v) { v = __shfl_sync(0xffffffffu, v, l_e); };
+        from(x.b), from(x.r0), from(x.nr), from(x.kl), from(x.ql), from(x.lo), from(x.hi), from(x.all_lo), from(x.all_hi), from(x.units);
+    } else {
         int a = 0, z = p.E;          // pre[a] <= u0 < pre[z]
         while (z - a > 1) {
             const int m = (a + z) >> 1;
             if (pre[m] <= u0) a = m; else z = m;
         }
         l_e = a;
+        x = entry_of<RB>(p, l_e);
     }
-    Entry x = entry_of<RB>(p, l_e);  // of the current segment
     int seg_h, seg_k;                // its head, and the first of its units in the item
     {
         const int in = u0 - pre[l_e];
@@ -677,11 +695,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             };
             const int cf = holder(item_first), cl = holder(item_first + x.units - 1);
             __syncthreads();
-            if (tid == 0) {
-                __threadfence();                 // after the barrier: of all the CTA's writes
-                misc[0] = arrive_last(word, found, p.ticket, cl - cf + 1) ? 1 : 0;
-                __threadfence();
-            }
+            if (tid == 0) misc[0] = arrive_last(word, found, p.ticket, cl - cf + 1) ? 1 : 0;
             __syncthreads();
             if (misc[0]) {
                 // a CTA whose share starts inside the item has it first, else last: all but
@@ -714,13 +728,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                             if (c > cl) mc[i][e] = -INFINITY;
                         }
                 };
+                float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);       // the warp's first row, a CTA per lane
+                if (warp < nr && cf + lane <= cl) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(cf + lane) + warp) * 4));
                 fetch(cf + gi);
                 // statistics of each row: a warp per row, a lane per CTA
                 float* const fin = st_max;       // [RB] merged max, [RB] 1 / merged sum (the warps' own are used up)
                 for (int rr = warp; rr < nr; rr += kWarps) {
                     float m = -INFINITY, lr = 0.f, l = 0.f;
                     for (int c = cf + lane; c <= cl; c += 32) {
-                        const float4 ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(c) + rr) * 4));
+                        if (rr != warp || c != cf + lane) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(c) + rr) * 4));
                         const float n = fmaxf(m, ml.x);
                         const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
                         const float h = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - n);

@@ -73,18 +73,15 @@ struct Rows {
     const int32_t* q_lens;     // or NULL: N_q
     int N_q, R;                // R = G * N_q
     int causal;
-    int window;                // < 0: none
+    int window;                // < 0: none; at most 2^30, as keys are, so that positions stay within int
 };
 
 // Keys [lo, hi) that a row of a sequence with kl keys and ql queries sees (hi <= lo: none).
 __device__ __forceinline__ void row_keys(const Rows& p, int kl, int ql, int row, int& lo, int& hi) {
     const int i = p.N_q == 1 ? 0 : row % p.N_q;
-    const long long at = (long long)kl - ql + i;
-    long long l = 0, h = (row < p.R && i < ql) ? kl : 0;
-    if (p.causal) h = min(h, at + 1);
-    if (p.window >= 0) l = max(l, at - p.window);
-    lo = (int)min(l, 0x7fffffffLL);
-    hi = (int)max(h, 0LL);
+    const int at = kl - ql + i;
+    lo = p.window >= 0 ? max(0, at - p.window) : 0;
+    hi = row < p.R && i < ql ? (p.causal ? max(0, min(kl, at + 1)) : kl) : 0;
 }
 
 // What a block of rows of a sequence attends to.
@@ -115,22 +112,14 @@ __device__ __forceinline__ Entry entry_of_rows(const Rows& p, const Paging& pg, 
     }
     const bool rows_without = i1 >= x.ql;
     i1 = min(i1, x.ql - 1);
-    const long long off = (long long)x.kl - x.ql;
-    long long lo = 0, hi = i0 > i1 ? 0 : x.kl, all_lo = 0, all_hi = rows_without ? 0 : x.kl;
-    if (p.causal) {
-        hi = min(hi, off + i1 + 1);
-        all_hi = min(all_hi, off + i0 + 1);
-    }
+    const int off = x.kl - x.ql;
+    x.hi = i0 > i1 ? 0 : (p.causal ? max(0, min(x.kl, off + i1 + 1)) : x.kl);
+    x.all_hi = rows_without ? 0 : (p.causal ? max(0, min(x.kl, off + i0 + 1)) : x.kl);
+    x.lo = x.all_lo = 0;
     if (p.window >= 0) {
-        lo = max(lo, off + i0 - p.window);
-        all_lo = max(all_lo, off + i1 - p.window);
+        x.lo = min(max(0, off + i0 - p.window), x.hi) & ~(kTile - 1);
+        x.all_lo = max(0, off + i1 - p.window);
     }
-    hi = max(hi, 0ll);
-    lo = min(lo, hi);
-    x.lo = (int)lo & ~(kTile - 1);
-    x.hi = (int)hi;
-    x.all_lo = (int)all_lo;
-    x.all_hi = (int)max(all_hi, 0ll);
     x.units = max(1, (x.hi - x.lo + kUnit - 1) / kUnit);
     return x;
 }
