@@ -614,8 +614,7 @@ int launch_rows(const CUtensorMap& tq, const CUtensorMap& to, const fa::kv4::Row
     });
     if (set[dev] != cudaSuccess) return ::cuda_fail("cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", set[dev]);
     const dim3 grid((unsigned)((p.rows.R + fa::kBlockM - 1) / fa::kBlockM), (unsigned)p.H_kv, (unsigned)B);
-    fa::kv4::rows_kernel<D, kOneRun><<<grid, fa::kv4::kRowsThreads, smem, stream>>>(tq, to, p);
-    e = cudaGetLastError();
+    e = launch_overlapped(fa::kv4::rows_kernel<D, kOneRun>, grid, fa::kv4::kRowsThreads, smem, stream, tq, to, p);
     return e == cudaSuccess ? FA_OK : ::cuda_fail("kernel launch (4-bit cache attention, many rows)", e);
 }
 }  // namespace

@@ -25,4 +25,21 @@ int ready_device(int* dev, int* num_sms);
 // SM count of the current device; 148 (a B200) where none is visible.
 int current_num_sms();
 
+// Launches a kernel that may be set up while the one before it on the stream still runs
+// (programmatic dependent launch): it calls fa::kv4::after_previous() before it touches memory.
+template <typename... P, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace fa_internal

@@ -17,6 +17,7 @@
 namespace {
 
 using fa_internal::cuda_fail;
+using fa_internal::launch_overlapped;
 using fa_internal::ready_device;
 namespace kv4 = fa::kv4;
 
@@ -133,12 +134,10 @@ int prepare_attend(int dev) {
 }
 
 template <int D, int NB>
-void launch_attend(const kv4::AttendParams& p, int num_sms, cudaStream_t s) {
-    const int grid = num_sms * ctas_per_sm(8 * NB);
-    if (p.pg.page_size % kv4::kTile == 0)
-        kv4::attend_kernel<D, NB, true><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
-    else
-        kv4::attend_kernel<D, NB, false><<<grid, kv4::kThreads, kv4::Cfg<D, NB>::kSmemBytes, s>>>(p);
+cudaError_t launch_attend(const kv4::AttendParams& p, int num_sms, cudaStream_t s) {
+    const int grid = num_sms * ctas_per_sm(8 * NB), smem = kv4::Cfg<D, NB>::kSmemBytes;
+    return launch_overlapped(p.pg.page_size % kv4::kTile == 0 ? kv4::attend_kernel<D, NB, true> : kv4::attend_kernel<D, NB, false>,
+                             grid, kv4::kThreads, smem, s, p);
 }
 
 }  // namespace
@@ -175,8 +174,7 @@ int fa_kv4_append(const void* k, const void* v, void* k_codes, void* k_scales, v
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const auto kernel = d == 64 ? (flat ? kv4::append_kernel<64, true> : kv4::append_kernel<64, false>)
                                 : (flat ? kv4::append_kernel<128, true> : kv4::append_kernel<128, false>);
-    kernel<<<grid, kv4::kRowThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(kernel, grid, kv4::kRowThreads, 0, s, p);
     return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache append)", e);
 }
 
@@ -210,8 +208,7 @@ int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const auto kernel = d == 64 ? (flat ? kv4::read_kernel<64, true> : kv4::read_kernel<64, false>)
                                 : (flat ? kv4::read_kernel<128, true> : kv4::read_kernel<128, false>);
-    kernel<<<grid, kv4::kRowThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(kernel, grid, kv4::kRowThreads, 0, s, p);
     return e == cudaSuccess ? FA_OK : cuda_fail("kernel launch (4-bit cache read)", e);
 }
 
@@ -295,11 +292,8 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
         p.rb0 = (int)(e0 % p.row_blocks);
         p.E = (int)std::min(chunk, entries - e0);
         p.ticket = next_ticket();
-        if (d == 64)
-            rb == 8 ? launch_attend<64, 1>(p, sms, s) : launch_attend<64, 2>(p, sms, s);
-        else
-            rb == 8 ? launch_attend<128, 1>(p, sms, s) : launch_attend<128, 2>(p, sms, s);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = d == 64 ? (rb == 8 ? launch_attend<64, 1>(p, sms, s) : launch_attend<64, 2>(p, sms, s))
+                                      : (rb == 8 ? launch_attend<128, 1>(p, sms, s) : launch_attend<128, 2>(p, sms, s));
         if (e != cudaSuccess) return cuda_fail("kernel launch (4-bit cache attention)", e);
     }
     return FA_OK;

@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;       // MMA fragment coordinates
 
+    after_previous();
+
     // ------------------------------------------------ the line of units
     Entry x;                         // of the current segment; first, of the thread's own entry
     const bool few = p.E <= 32;      // then every warp makes the line by itself, an entry per lane

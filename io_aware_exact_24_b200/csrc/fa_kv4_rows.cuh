@@ -116,8 +116,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // rows that see more keys (causal: the later ones of a head) start first
     const int m0 = (int)(gridDim.x - 1 - blockIdx.x) * kBlockM;
     const int h = blockIdx.y, b = blockIdx.z;
-    const Entry x = entry_of_rows<kBlockM, 32, kBlockN>(p.rows, p.pg, b, m0);
-    const int n_kv = x.hi > x.lo ? x.units : 0;
 
     // ---- setup
     if (warp == kProducerWarp && lane == 0) {
@@ -153,6 +151,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         sts16(a, F::kOnesWord, F::kOnesWord, F::kOnesWord, F::kOnesWord);
     }
     fence_proxy_async_smem();
+    after_previous();
+    const Entry x = entry_of_rows<kBlockM, 32, kBlockN>(p.rows, p.pg, b, m0);
+    const int n_kv = x.hi > x.lo ? x.units : 0;
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
