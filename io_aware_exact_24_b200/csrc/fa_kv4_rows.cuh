@@ -10,7 +10,7 @@
 // bf16 copy of the cache passes through memory.
 //
 // The codes of a 32-bit word come out as channels (0,4) (1,5) (2,6) (3,7).  K is stored in
-// that order, Q is brought into it once per CTA, and of O, whose columns follow V's, the
+// that order, Q goes to TMEM in it, and of O, whose columns follow V's, the
 // epilogue picks the columns back.
 //
 // A NaN group of V would reach the rows that do not see its key as 0 * NaN: it is stored as
@@ -40,8 +40,15 @@ static_assert(kNotes >= fa::Cfg<64>::kStagesK + 3 && kNotes >= fa::Cfg<128>::kSt
 template <int D>
 struct RowsCfg {
     using F = fa::Cfg<D>;
-    // barriers: q_full, q_ready, then per ring full and empty, s_full[2], s_free, p_full[3], pv_done[3], drain
-    static constexpr int kNumBars = 2 + 2 * F::kStages + 2 + 1 + 3 + 3 + 1;
+    // TMEM: the scores, two P buffers, O with its row sums (and 16 unused columns that the
+    // rescale touches), and Q: as the A operand it would be read from shared memory once per
+    // tile, whose bandwidth the tiles' making takes
+    static constexpr int kPBufs = 2;
+    __host__ __device__ static constexpr uint32_t col_p(int b) { return 128u + 64u * b; }
+    static constexpr uint32_t kColO = 128u + 64u * kPBufs, kColL = kColO + D, kColQ = kColL + 32;
+    static_assert(kColQ + D / 2 <= 512, "TMEM columns");
+    // barriers: q_full, q_ready, then per ring full and empty, s_full[2], s_free, p_full, pv_done, drain
+    static constexpr int kNumBars = 2 + 2 * F::kStages + 2 + 1 + 2 * kPBufs + 1;
     static constexpr int kBarOff = F::kBarOff;
     static constexpr int kMiscOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // tmem base, abort flag
     static constexpr int kMrefOff = kMiscOff + 16;
@@ -50,13 +57,13 @@ struct RowsCfg {
     // groups), then its 32 keys' NaN bits per group
     static constexpr int kNoteBytes = kMakers * 4 * (1 + D / kGroup);
     static constexpr int kNoteOff = kEpiOff + 3 * kGroups * kBlockM * 4;
-    // staging of the codes: per maker warp, pass and lane 16 bytes of K, 16 of V, 4 of scales of each
+    // staging of a maker warp: 16 bytes of K's codes and of V's per pass and lane, then its 32
+    // keys' scales of K and of V
     static constexpr int kPass = D / kGroup;
     static constexpr int kStageOff = (kNoteOff + kNotes * kNoteBytes + 15) / 16 * 16;
     static constexpr int kStageV = kPass * 32 * 16;
-    static constexpr int kStageKS = 2 * kStageV;
-    static constexpr int kStageVS = kStageKS + kPass * 32 * 4;
-    static constexpr int kStageWarp = kStageVS + kPass * 32 * 4;
+    static constexpr int kStageS = 2 * kStageV;
+    static constexpr int kStageWarp = kStageS + 2 * 32 * (D / kGroup) * 2;
     static constexpr int kSmemBytes = kStageOff + kMakers * kStageWarp + 1024;
     static_assert(kSmemBytes <= 232448 && kSmemBytes > 116 * 1024, "one CTA per SM");
 };
@@ -75,12 +82,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int D, bool kOneRun>
@@ -100,8 +103,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     auto bar_s_full = [&](int g) { return bar(2 + 2 * F::kStages + g); };
     const uint32_t bar_s_free = bar(4 + 2 * F::kStages);
     auto bar_p_full = [&](int b) { return bar(5 + 2 * F::kStages + b); };
-    auto bar_pv_done = [&](int b) { return bar(8 + 2 * F::kStages + b); };
-    const uint32_t bar_drain = bar(11 + 2 * F::kStages);
+    auto bar_pv_done = [&](int b) { return bar(5 + C::kPBufs + 2 * F::kStages + b); };
+    const uint32_t bar_drain = bar(5 + 2 * C::kPBufs + 2 * F::kStages);
     uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
     const uint32_t mref_w = base + C::kMrefOff;
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // ---- setup
     if (warp == kProducerWarp && lane == 0) {
         mbar_init(bar_q_full, 1);
-        mbar_init(bar_q_ready, kMakers);
+        mbar_init(bar_q_ready, D / 16);          // one warp per lane quadrant and 32 columns
         for (int r = 0; r < 2; ++r)
             for (int s = 0; s < (r == 0 ? F::kStagesK : F::kStagesV); ++s) {
                 mbar_init(bar_full(r, s), kMakers);
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         mbar_init(bar_s_full(0), 1);
         mbar_init(bar_s_full(1), 1);
         mbar_init(bar_s_free, 4);
-        for (int i = 0; i < F::kPBufs; ++i) {
+        for (int i = 0; i < C::kPBufs; ++i) {
             mbar_init(bar_p_full(i), 4);
             mbar_init(bar_pv_done(i), 1);
         }
@@ -192,29 +195,46 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) row[i] = __shfl_sync(0xffffffffu, l_row[i], j & 31);
         };
+        // where this lane's chunks lie behind a run's first row
+        constexpr int kRow = D / 2, kSRow = kG * 2, kRunKeys = 32 / kRuns, kRunPass = kPass / kRuns;
+        const uint8_t* const src_k = p.k_codes + key_l * kRow + grp * 16;
+        const uint8_t* const src_v = p.v_codes + key_l * kRow + grp * 16;
+        constexpr int kSC = 32 * kSRow / 16;         // 16-byte chunks of the warp's scales, per tensor: 16 or 8
+        const int s_chunk = lane % kSC, s_run = s_chunk / (kSC / kRuns);
+        const uint8_t* const src_s = reinterpret_cast<const uint8_t*>(lane < kSC ? p.k_scales : p.v_scales) + s_chunk % (kSC / kRuns) * 16;
         auto copy_k = [&]() {            // K and both scales of the rows just looked up
+            uint32_t s_row = row[0];
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) {
-                const int i = o * kKeys / 16 % kRuns, in = o * kKeys - (kOneRun ? 0 : i * 16);
+            for (int i = 0; i < kRuns; ++i) {
+                if (i == s_run) s_row = row[i];
                 if (row[i] != 0xffffffffu) {
-                    const size_t r = row[i] + (uint32_t)(in + key_l);
-                    cp_async<16>(stage + (uint32_t)((o * 32 + lane) * 16), p.k_codes + r * (D / 2) + grp * 16);
-                    cp_async<4>(stage + (uint32_t)(C::kStageKS + (o * 32 + lane) * 4), p.k_scales + r * kG + (grp & ~1));
-                    cp_async<4>(stage + (uint32_t)(C::kStageVS + (o * 32 + lane) * 4), p.v_scales + r * kG + (grp & ~1));
+                    const uint8_t* const src = src_k + (size_t)row[i] * kRow;
+#pragma unroll
+                    for (int o = 0; o < kRunPass; ++o)
+                        cp_async16(stage + (uint32_t)(((i * kRunPass + o) * 32 + lane) * 16), src + o * kKeys * kRow);
                 }
             }
+            if (s_row != 0xffffffffu && lane < 2 * kSC)
+                cp_async16(stage + (uint32_t)(C::kStageS + lane * 16), src_s + (size_t)s_row * kSRow);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto copy_v = [&](const uint32_t (&vr)[kRuns]) {
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) {
-                const int i = o * kKeys / 16 % kRuns, in = o * kKeys - (kOneRun ? 0 : i * 16);
-                if (vr[i] != 0xffffffffu)
-                    cp_async<16>(stage + (uint32_t)(C::kStageV + (o * 32 + lane) * 16),
-                                 p.v_codes + (size_t)(vr[i] + (uint32_t)(in + key_l)) * (D / 2) + grp * 16);
-            }
+            for (int i = 0; i < kRuns; ++i)
+                if (vr[i] != 0xffffffffu) {
+                    const uint8_t* const src = src_v + (size_t)vr[i] * kRow;
+#pragma unroll
+                    for (int o = 0; o < kRunPass; ++o)
+                        cp_async16(stage + (uint32_t)(C::kStageV + ((i * kRunPass + o) * 32 + lane) * 16), src + o * kKeys * kRow);
+                }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        auto lds2 = [](uint32_t a) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+            return (uint32_t)v;
+        };
+        const uint32_t at_s = stage + (uint32_t)(C::kStageS + key_l * kSRow + grp * 2);
         auto store = [&](uint32_t slot, int o, const uint4& c, uint32_t s) {
             const uint32_t s2 = __byte_perm(s, s, 0x1010), z2 = minus_24(s2);
             const int key = w * 32 + o * kKeys + key_l;
@@ -225,94 +245,95 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 sts16(at + (uint32_t)(((((grp & 1) << 2) + i) ^ (key & 7)) << 4), codes_to_bf16x2(0, word[i], s2, z2),
                       codes_to_bf16x2(1, word[i], s2, z2), codes_to_bf16x2(2, word[i], s2, z2), codes_to_bf16x2(3, word[i], s2, z2));
         };
-        if (n_kv > 0) {
-            rows_of(0);
-            copy_k();
-            copy_v(row);
-            // Q into the order of the codes: row 32w + lane
-            ok = __all_sync(0xffffffffu, wait_bounded(bar_q_full, 0, abort_flag, p.wait_limit));
-            if (ok) {
-                const uint32_t row = q_tile + (uint32_t)(w * 32 + lane) * 128u;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t a = row + (uint32_t)((i >> 3) * F::kBoxBytes + (((i & 7) ^ (lane & 7)) << 4));
-                    const uint4 v = code_order(lds16(a));
-                    sts16(a, v.x, v.y, v.z, v.w);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_q_ready);
-            }
-        }
-        for (int j = 0; j < n_kv && ok; ++j) {
-            const int sk = j % F::kStagesK, sv = j % F::kStagesV;
-            uint32_t here[kRuns];        // of this tile; row moves on to the next one
+        // K tiles are made one ahead of V tiles: a V slot is free only when the tile two before has
+        // been through the softmax, and the next scores should not wait for that.
+        uint32_t v_row[kRuns];           // of the V tile to make next
+        uint32_t v_sc[kPass];            // and its scales
+        auto make_k = [&](int j) {       // makes K of the tile whose copies are complete, and starts the next one's
+            const int sl = j % F::kStagesK;
             uint32_t gone = 0;           // runs that are not there
+            uint4 cw[kPass];
+            uint32_t sc[kPass];
+            bool bad = false;
+            const int left = x.kl - (x.lo + j * kBlockN + w * 32 + key_l);   // keys of the sequence from the lane's first on
+            __syncwarp();                // the scales are other lanes' copies
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
-                here[i] = row[i];
-                if (here[i] == 0xffffffffu) gone |= kOneRun ? 3u : 1u << i;
+                v_row[i] = row[i];
+                if (row[i] == 0xffffffffu) gone |= kOneRun ? 3u : 1u << i;
             }
-            uint4 cw[kPass];
-            uint32_t sc[kPass];          // K's scale in the low half, V's in the high one
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            // a run that is not there gives whatever is in the staging: its scores are masked, and
+            // its V, as that of rows behind the last key, which may hold anything, counts as zero
 #pragma unroll
             for (int o = 0; o < kPass; ++o) {
-                const int i = o * kKeys / 16 % kRuns;
-                cw[o] = make_uint4(0, 0, 0, 0);
-                sc[o] = 0;
-                if (here[i] != 0xffffffffu) {
-                    cw[o] = lds16(stage + (uint32_t)((o * 32 + lane) * 16));
-                    uint32_t ks, vs;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ks) : "r"(stage + (uint32_t)(C::kStageKS + (o * 32 + lane) * 4)));
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(stage + (uint32_t)(C::kStageVS + (o * 32 + lane) * 4)));
-                    // rows behind the last key may hold anything: their V counts as zero
-                    if (x.lo + j * kBlockN + w * 32 + o * kKeys + key_l >= x.kl) vs = 0;
-                    sc[o] = __byte_perm(ks, vs, (grp & 1) ? 0x7632 : 0x5410);
-                }
+                cw[o] = lds16(stage + (uint32_t)((o * 32 + lane) * 16));
+                sc[o] = lds2(at_s + o * kKeys * kSRow);
+                v_sc[o] = lds2(at_s + 32 * kSRow + o * kKeys * kSRow);
+                if (o * kKeys >= left || row[o / kRunPass] == 0xffffffffu) v_sc[o] = 0;
+                bad |= (v_sc[o] & 0x7f80u) == 0x7f80u;
             }
+            __syncwarp();
             if (j + 1 < n_kv) rows_of(j + 1);
             else
 #pragma unroll
                 for (int i = 0; i < kRuns; ++i) row[i] = 0xffffffffu;
             copy_k();
-            ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(0, sk), ((uint32_t)(j / F::kStagesK) & 1u) ^ 1u, abort_flag, p.wait_limit));
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, wait_bounded(bar_empty(0, sl), ((uint32_t)(j / F::kStagesK) & 1u) ^ 1u, abort_flag, p.wait_limit)))
+                return false;
             // notes first: whoever sees this tile's scores sees them too
-            uint32_t bad = 0;
-#pragma unroll
-            for (int o = 0; o < kPass; ++o) bad |= ((sc[o] >> 16) & 0x7f80u) == 0x7f80u ? 1u << o : 0u;
-            const bool any_bad = __any_sync(0xffffffffu, bad != 0);
+            const bool any_bad = __any_sync(0xffffffffu, bad);
             if (any_bad) {
                 uint32_t word = 0;           // lane g's: the 32 keys' bits of group g
 #pragma unroll
                 for (int o = 0; o < kPass; ++o) {
-                    const uint32_t bal = __ballot_sync(0xffffffffu, (bad >> o) & 1u);
+                    const bool is = (v_sc[o] & 0x7f80u) == 0x7f80u;
+                    const uint32_t bal = __ballot_sync(0xffffffffu, is);
                     if (lane < kG) word |= ((bal >> (lane * kKeys)) & ((1u << kKeys) - 1u)) << (o * kKeys);
-                    if ((bad >> o) & 1u) sc[o] &= 0xffffu;
+                    if (is) v_sc[o] = 0;
                 }
                 if (lane < kG) note(j)[kMakers + w * kG + lane] = word;
             }
             if (lane == 0) note(j)[w] = gone | (any_bad ? 4u : 0u);
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sk), o, cw[o], sc[o]);
+            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sl), o, cw[o], sc[o]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_full(0, sk));
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (lane == 0) mbar_arrive(bar_full(0, sl));
+            return true;
+        };
+        if (n_kv > 0) {
+            rows_of(0);
+            copy_k();
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            ok = make_k(0);
+            copy_v(v_row);
+        }
+        for (int j = 0; j < n_kv && ok; ++j) {
+            const int sl = j % F::kStagesV;
+            uint4 cw[kPass];
+            uint32_t sc[kPass];
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) {
-                cw[o] = make_uint4(0, 0, 0, 0);
-                if (here[o * kKeys / 16 % kRuns] != 0xffffffffu) cw[o] = lds16(stage + (uint32_t)(C::kStageV + (o * 32 + lane) * 16));
-            }
-            copy_v(row);
-            ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(1, sv), ((uint32_t)(j / F::kStagesV) & 1u) ^ 1u, abort_flag, p.wait_limit));
+            for (int o = 0; o < kPass; ++o) sc[o] = v_sc[o];
+            asm volatile("cp.async.wait_group 1;" ::: "memory");     // K of tile j + 1
+            if (j + 1 < n_kv)
+                ok = make_k(j + 1);
+            else
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            if (!ok) break;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");     // V of tile j
+#pragma unroll
+            for (int o = 0; o < kPass; ++o) cw[o] = lds16(stage + (uint32_t)(C::kStageV + (o * 32 + lane) * 16));
+            if (j + 1 >= n_kv)
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) v_row[i] = 0xffffffffu;
+            copy_v(v_row);
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(1, sl), ((uint32_t)(j / F::kStagesV) & 1u) ^ 1u, abort_flag, p.wait_limit));
             if (!ok) break;
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sv), o, cw[o], sc[o] >> 16);
+            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sl), o, cw[o], sc[o]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_full(1, sv));
+            if (lane == 0) mbar_arrive(bar_full(1, sl));
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");   // nothing lands after the CTA's end
         __syncwarp();
@@ -331,6 +352,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 bool ok = true;
                 if (warp == kMmaWarp) {
                     ok = wait_bounded(bar_q_ready, 0, abort_flag, p.wait_limit);
+                    tc_fence_after();
                     for (int i = 0; i < n_kv && ok; ++i) {
                         if (i > 0) ok = wait_bounded(bar_s_free, (uint32_t)((i - 1) & 1), abort_flag, p.wait_limit);
                         const int sl = i % F::kStagesK;
@@ -341,23 +363,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t koff = (uint32_t)((kk / 4) * F::kBoxBytes + (kk % 4) * 32);
-                            umma_ss(tmem + F::col_s(0), smem_desc_sw128(q_tile + koff, 16, 1024),
-                                    smem_desc_sw128(slot + koff, 16, 1024), F::kIdescQK, kk > 0 ? 1u : 0u);
+                            umma_ts(tmem + F::col_s(0), tmem + C::kColQ + (uint32_t)(kk * 8), smem_desc_sw128(slot + koff, 16, 1024),
+                                    F::kIdescQK, kk > 0 ? 1u : 0u);
                         }
                         umma_commit(bar_s_full(i & 1));
                         umma_commit(bar_empty(0, sl));
                     }
                 } else {
                     for (int j = 0; j < n_kv && ok; ++j) {
-                        const int pb = j % F::kPBufs, sl = j % F::kStagesV;
-                        ok = wait_bounded(bar_p_full(pb), (uint32_t)((j / F::kPBufs) & 1), abort_flag, p.wait_limit);
+                        const int pb = j % C::kPBufs, sl = j % F::kStagesV;
+                        ok = wait_bounded(bar_p_full(pb), (uint32_t)((j / C::kPBufs) & 1), abort_flag, p.wait_limit);
                         if (ok) ok = wait_bounded(bar_full(1, sl), (uint32_t)((j / F::kStagesV) & 1), abort_flag, p.wait_limit);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t slot = ring_slot(1, sl);
 #pragma unroll
                         for (int kk = 0; kk < kBlockN / 16; ++kk)
-                            umma_ts(tmem + F::kColO, tmem + F::col_p(pb) + (uint32_t)(kk * 8),
+                            umma_ts(tmem + C::kColO, tmem + C::col_p(pb) + (uint32_t)(kk * 8),
                                     smem_desc_sw128(slot + (uint32_t)(kk * 16 * 128), F::kBoxBytes, 1024), F::kIdescPV,
                                     (j > 0 || kk > 0) ? 1u : 0u);
                         umma_commit(bar_pv_done(pb));
@@ -384,7 +406,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         float m_seen = -INFINITY, lu = 0.f;
         uint32_t nan_groups = 0;         // groups of V that a key this row sees holds as NaN
         bool ok = true;
-        for (int j = g; j < n_kv; j += 2) {
+        if (n_kv > 0 && 32 * g < D / 2) {
+            // Q into TMEM, in the order of the codes: columns 32g .. 32g + 31 of this row
+            ok = __all_sync(0xffffffffu, wait_bounded(bar_q_full, 0, abort_flag, p.wait_limit));
+            if (ok) {
+                uint32_t u[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = code_order(lds16(q_tile + (uint32_t)(g * F::kBoxBytes + r * 128 + ((i ^ (r & 7)) << 4))));
+                    u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+                }
+                tmem_st32(tmem + lane_off + C::kColQ + 32u * g, u);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_q_ready);
+            }
+        }
+        for (int j = g; j < n_kv && ok; j += 2) {
             bool good = wait_bounded(bar_s_full(g), (uint32_t)((j >> 1) & 1), abort_flag, p.wait_limit);
             if (!__all_sync(0xffffffffu, good)) {
                 ok = false;
@@ -450,9 +489,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 m_seen = m_cur;
             }
             const float mu = (m_cur == -INFINITY) ? 0.f : m_cur;
-            const int pb = j % F::kPBufs;
-            if (j >= F::kPBufs) {
-                good = wait_bounded(bar_pv_done(pb), (uint32_t)(((j - F::kPBufs) / F::kPBufs) & 1), abort_flag, p.wait_limit);
+            const int pb = j % C::kPBufs;
+            if (j >= C::kPBufs) {
+                good = wait_bounded(bar_pv_done(pb), (uint32_t)(((j - C::kPBufs) / C::kPBufs) & 1), abort_flag, p.wait_limit);
                 if (!__all_sync(0xffffffffu, good)) {
                     ok = false;
                     break;
@@ -460,13 +499,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             // (all on MUFU: the polynomial of the dense forward would lose a NaN)
             float2 lu2 = make_float2(0.f, 0.f);
-            const uint32_t taddr_p = tmem + lane_off + F::col_p(pb);
+            const uint32_t taddr_p = tmem + lane_off + C::col_p(pb);
             exp_store_half<0, 0>(s, c, mu, taddr_p, lu2);
             exp_store_half<0, 1>(s, c, mu, taddr_p, lu2);
             lu += lu2.x + lu2.y;
             const float alpha = (m_cur != m_prev) ? ex2_approx(m_prev - m_cur) : 1.f;
             if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                good = wait_bounded(bar_pv_done((j - 1) % F::kPBufs), (uint32_t)(((j - 1) / F::kPBufs) & 1), abort_flag, p.wait_limit);
+                good = wait_bounded(bar_pv_done((j - 1) % C::kPBufs), (uint32_t)(((j - 1) / C::kPBufs) & 1), abort_flag, p.wait_limit);
                 if (!__all_sync(0xffffffffu, good)) {
                     tmem_wait_st();
                     ok = false;
@@ -475,7 +514,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int q4 = 0; q4 < D / 32 + 1; ++q4) {   // O and its row-sum columns
-                    const uint32_t ocol = tmem + lane_off + F::kColO + 32u * q4;
+                    const uint32_t ocol = tmem + lane_off + C::kColO + 32u * q4;
                     uint32_t u[32];
                     tmem_ld32(ocol, u);
                     tmem_wait_ld();
@@ -514,7 +553,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             float l_row = 0.f;
             if (have_o) {
                 uint32_t u[32];
-                tmem_ld32(tmem + lane_off + F::kColL, u);
+                tmem_ld32(tmem + lane_off + C::kColL, u);
                 tmem_wait_ld();
                 reg_after_wait(u[0]);
                 l_row = __uint_as_float(u[0]);
@@ -526,7 +565,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 const float inv_l = ((nan_groups >> (col0 / kGroup)) & 1u) ? __int_as_float(0x7fc00000) : inv_row;
                 uint32_t u[32];
                 if (have_o) {
-                    tmem_ld32(tmem + lane_off + F::kColO + (uint32_t)col0, u);
+                    tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)col0, u);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) reg_after_wait(u[i]);
