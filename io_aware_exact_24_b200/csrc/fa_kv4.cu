@@ -91,7 +91,7 @@ int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::C
 // 512 rows 103 and 95 us; 64 heads, 4096 keys, 64 rows 57 and 58 us, 128 rows 57 and 101 us.
 bool many_rows(long long R, long long heads, int num_sms) {
     const long long waves = ((R + 127) / 128 * heads + num_sms - 1) / num_sms;
-    return R > 16 && 84 * ((R + 15) / 16) * heads > 160 * waves * num_sms;
+    return R > 16 && 84 * ((R + 15) / 16) * heads > 130 * waves * num_sms;
 }
 
 // Workspace of the attention: two partial results per CTA, then the arrival words.

@@ -98,22 +98,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+// Plain loads, which the compiler may move between the barriers.
 template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
-    if constexpr (W == 4)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(addr));
-    else if constexpr (W == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[W]) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
+__device__ __forceinline__ uint32_t lds_u16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
 // Arrivals of a call's CTAs at an item.  The word holds (ticket << 16) | count, and 0 after
 // a call.  At its segment's start a CTA tries to claim a 0 for this call's ticket; one that
@@ -274,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             }
         }
     };
-    const uint32_t ring = base + (uint32_t)(warp * C::kStages * C::kStageBytes);
+    const uint32_t ring = (uint32_t)(warp * C::kStages * C::kStageBytes);
     // Rows and chunks of 16 bytes are placed so that the fragment loads below are free of
     // bank conflicts: the lanes that one shared-memory access serves hit different banks.
     constexpr int kPer = C::kRow / 16;            // chunks of a token's codes: 4 or 2
@@ -320,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                 const uint8_t* const v = src_v + (size_t)row[i] * C::kRow;
 #pragma unroll
                 for (int j = 0; j < 2 / kRuns * (C::kRow / 32); ++j) {   // 16 keys: kRow / 32 chunks a lane
-                    cp_async16(st + dst_k + i * 16 * C::kRow + j * 512, k + j * 512);
-                    cp_async16(st + dst_v + i * 16 * C::kRow + j * 512, v + j * 512);
+                    cp_async16(base + st + dst_k + i * 16 * C::kRow + j * 512, k + j * 512);
+                    cp_async16(base + st + dst_v + i * 16 * C::kRow + j * 512, v + j * 512);
                 }
-                if (s_run == i) cp_async16(st + dst_s, src_s + (size_t)row[i] * C::kSRow);
+                if (s_run == i) cp_async16(base + st + dst_s, src_s + (size_t)row[i] * C::kSRow);
             }
         cp_async_commit();
         ++l_at;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     float ref[NB][2];                // reference max of rows 2t, 2t + 1 (log2 units), equal in all lanes of a t
     float top[NB][2];                // raw score above which the reference moves
     float neg[NB][2];                // -ref, or 0 while the row has seen no key
-    const uint32_t qs = base + C::kQOff + lane * 16;
+    uint8_t* const qs = smem + C::kQOff + lane * 16;
     // MMA row i of a 16-key tile (i < 8) is key i/2 + 4 (i mod 2), row 8 + i that key + 8
     const int key0 = (g >> 1) + 4 * (g & 1);
     const uint32_t at_k = (uint32_t)((D == 128 ? key0 ^ ((key0 >> 2) & 1) : key0 ^ (((key0 >> 2) & 1) << 1)) * C::kRow +
@@ -387,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) s[j][nb][0] = s[j][nb][1] = s[j][nb][2] = s[j][nb][3] = 0.f;
-            lds_words<kKW>(st + at_k + j * 16 * C::kRow, w0[j]);
-            lds_words<kKW>(st + at_k + (j * 16 + 8) * C::kRow, w1[j]);
-            s0[j] = lds_u16(st + at_ks + j * 16 * C::kSRow);
-            s1[j] = lds_u16(st + at_ks + (j * 16 + 8) * C::kSRow);
+            lds_words<kKW>(smem + st + at_k + j * 16 * C::kRow, w0[j]);
+            lds_words<kKW>(smem + st + at_k + (j * 16 + 8) * C::kRow, w1[j]);
+            s0[j] = lds_u16(smem + st + at_ks + j * 16 * C::kSRow);
+            s1[j] = lds_u16(smem + st + at_ks + (j * 16 + 8) * C::kSRow);
             s0[j] = __byte_perm(s0[j], s0[j], 0x1010);
             s1[j] = __byte_perm(s1[j], s1[j], 0x1010);
             z0[j] = minus_24(s0[j]);
@@ -480,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             uint32_t w[4][kVW], sv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                lds_words<kVW>(st + at_v + (j * 16 + 4 * i) * C::kRow, w[i]);
-                sv[i] = lds_u16(st + at_vs + (j * 16 + 4 * i) * C::kSRow);
+                lds_words<kVW>(smem + st + at_v + (j * 16 + 4 * i) * C::kRow, w[i]);
+                sv[i] = lds_u16(smem + st + at_vs + (j * 16 + 4 * i) * C::kSRow);
             }
             bool poisoned = false;
             if (edge) {
@@ -568,10 +566,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                 const int r = i / kKW * 8 + g, w = i % kKW;
                 const uint4 y = r < x.nr ? __ldg(reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4)) + w)
                                          : make_uint4(0, 0, 0, 0);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qs + i * 512),
-                             "r"(__byte_perm(y.x, y.z, 0x5410)), "r"(__byte_perm(y.x, y.z, 0x7632)),
-                             "r"(__byte_perm(y.y, y.w, 0x5410)), "r"(__byte_perm(y.y, y.w, 0x7632))
-                             : "memory");
+                *reinterpret_cast<uint4*>(qs + i * 512) =
+                    make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410),
+                               __byte_perm(y.y, y.w, 0x7632));
             }
         }
         if (tid < RB) {

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             for (int i = 0; i < kRuns; ++i) row[i] = __shfl_sync(0xffffffffu, l_row[i], j & 31);
         };
         // where this lane's chunks lie behind a run's first row
-        constexpr int kRow = D / 2, kSRow = kG * 2, kRunKeys = 32 / kRuns, kRunPass = kPass / kRuns;
+        constexpr int kRow = D / 2, kSRow = kG * 2, kRunPass = kPass / kRuns;
         const uint8_t* const src_k = p.k_codes + key_l * kRow + grp * 16;
         const uint8_t* const src_v = p.v_codes + key_l * kRow + grp * 16;
         constexpr int kSC = 32 * kSRow / 16;         // 16-byte chunks of the warp's scales, per tensor: 16 or 8
