@@ -81,8 +81,14 @@ unsigned long long next_ticket() {
     return t;
 }
 
-// Rows per block: one MMA column block holds 8 query rows.
-int row_block(long long R) { return R <= 8 ? 8 : 16; }
+// Rows per block.  One MMA column block holds 8 query rows; two share a dequantised operand,
+// at 0.84 us of an SM for 128 keys where one takes 0.6, but leave two CTAs to an SM instead of
+// three.  So 8 where a second block of 16 would be half empty (20 rows of 64 heads within a
+// window of 2048: 27 and 33 us; 4096 keys: 37 and 36), and where there is little work, when
+// latency counts (16 rows of 8 heads, 8192 keys: 19 and 25 us; of 64 heads, 4096: 29 and 28).
+int row_block(long long R, long long heads) {
+    return R <= 8 || (R > 16 && R <= 24) || (R <= 64 && heads * ((R + 15) / 16) <= 32) ? 8 : 16;
+}
 int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
 
 // Whether the kernel for many rows (fa_kv4_rows.cuh) is the quicker one.  Per 128 keys it takes
@@ -100,7 +106,7 @@ struct Layout {
 };
 Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
     const long long R = (long long)(H / H_kv) * N_q;
-    const int rb = row_block(R);
+    const int rb = row_block(R, (long long)B * H_kv);
     const size_t slots = 2 * (size_t)num_sms * ctas_per_sm(rb);
     const long long entries = (R + rb - 1) / rb * B;
     Layout L{};
@@ -266,7 +272,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
         p.scale_log2 = scale_log2;
         return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
     }
-    const int rb = row_block(R);
+    const int rb = row_block(R, (long long)B * H_kv);
     kv4::AttendParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k_codes = static_cast<const uint8_t*>(k_codes);
