@@ -122,7 +122,8 @@ def load_library() -> ctypes.CDLL:
             except ImportError as e:
                 raise ImportError("the _fastcall module is missing: build it with `python -m io_aware_exact_24_b200.build`") from e
             _fastcall.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)))
+                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)),
+                           _current_device)
             _fast = _fastcall
             _lib = lib
     return _lib
@@ -293,6 +294,12 @@ def fa_fwd_splitkv_noalloc(q, k, v, o, lse, B, H, N_q, N_k, d, scale, causal, ke
     if check and st != FA_OK:
         raise FaError(st, "fa_fwd_splitkv_noalloc")
     return st
+
+
+def _current_device() -> int:
+    """Number of the current device (0 where CUDA has not been used)."""
+    import torch
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _marshaller():

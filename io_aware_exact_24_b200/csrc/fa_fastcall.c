@@ -5,7 +5,8 @@
  * microseconds, as long as the kernels of a small step run.  The wrappers here take the same
  * arguments as those of binding.py and turn them into the same C calls: tensors (anything with
  * data_ptr()), integers and None become addresses, numbers become numbers.  They compute
- * nothing and link against nothing; init() hands them the entry points' addresses.
+ * nothing and link against nothing; init() hands them the entry points' addresses.  Of the
+ * tensors, the dense ones must be contiguous, and they and the cache on the current device.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -20,7 +21,16 @@ typedef int (*fwd_fn)(const void *, const void *, const void *, const void *, co
 
 static rows_fn g_append, g_read;
 static fwd_fn g_fwd;
-static PyObject *g_data_ptr;   /* "data_ptr" */
+static PyObject *g_data_ptr, *g_get_device, *g_is_contiguous;   /* names of a tensor's methods */
+static PyObject *g_current;                                     /* returns the current device */
+
+static int not_a_tensor(PyObject *x) {
+    if (PyErr_ExceptionMatches(PyExc_AttributeError)) {
+        PyErr_Clear();
+        PyErr_Format(PyExc_TypeError, "cannot take the address of %R", (PyObject *)Py_TYPE(x));
+    }
+    return 0;
+}
 
 /* Address of a tensor, an integer or None; -1 on success, else 0 with an exception set. */
 static int address(PyObject *x, void **out) {
@@ -33,16 +43,41 @@ static int address(PyObject *x, void **out) {
         return *out != NULL || !PyErr_Occurred() ? -1 : 0;
     }
     PyObject *a = PyObject_CallMethodNoArgs(x, g_data_ptr);
-    if (a == NULL) {
-        if (PyErr_ExceptionMatches(PyExc_AttributeError)) {
-            PyErr_Clear();
-            PyErr_Format(PyExc_TypeError, "cannot take the address of %R", (PyObject *)Py_TYPE(x));
-        }
-        return 0;
-    }
+    if (a == NULL) return not_a_tensor(x);
     *out = PyLong_AsVoidPtr(a);
     Py_DECREF(a);
     return *out != NULL || !PyErr_Occurred() ? -1 : 0;
+}
+
+/* A tensor given here must lie on the current device, and, where asked, be contiguous: the
+ * kernels would read other memory than it means, or fault.  Addresses are taken as they are. */
+static int tensor_ok(PyObject *x, int contiguous) {
+    if (x == Py_None || PyLong_Check(x)) return -1;
+    PyObject *d = PyObject_CallMethodNoArgs(x, g_get_device);
+    if (d == NULL) return not_a_tensor(x);
+    const long dev = PyLong_AsLong(d);
+    Py_DECREF(d);
+    PyObject *c = PyObject_CallNoArgs(g_current);
+    if (c == NULL) return 0;
+    const long cur = PyLong_AsLong(c);
+    Py_DECREF(c);
+    if (PyErr_Occurred()) return 0;
+    if (dev != cur) {
+        PyErr_Format(PyExc_ValueError, "a tensor is on device %ld, the current device is %ld (-1: the CPU)", dev, cur);
+        return 0;
+    }
+    if (contiguous) {
+        PyObject *r = PyObject_CallMethodNoArgs(x, g_is_contiguous);
+        if (r == NULL) return 0;
+        const int yes = PyObject_IsTrue(r);
+        Py_DECREF(r);
+        if (yes < 0) return 0;
+        if (!yes) {
+            PyErr_SetString(PyExc_ValueError, "a tensor is not contiguous");
+            return 0;
+        }
+    }
+    return -1;
 }
 
 static int number(PyObject *x, int *out) {
@@ -65,11 +100,12 @@ static int count_is(Py_ssize_t n, Py_ssize_t want) {
     return 0;
 }
 
-/* 9 addresses, 7 numbers, the stream */
-static PyObject *rows_call(rows_fn fn, PyObject *const *a, Py_ssize_t n) {
+/* 9 addresses, 7 numbers, the stream; a[dense] and a[dense + 1] are k and v, a[cache] a buffer of the cache */
+static PyObject *rows_call(rows_fn fn, PyObject *const *a, Py_ssize_t n, int dense, int cache) {
     void *p[9], *stream;
     int v[7], i;
     if (!count_is(n, 17)) return NULL;
+    if (!tensor_ok(a[dense], 1) || !tensor_ok(a[dense + 1], 1) || !tensor_ok(a[cache], 0)) return NULL;
     for (i = 0; i < 9; ++i)
         if (!address(a[i], &p[i])) return NULL;
     for (i = 0; i < 7; ++i)
@@ -82,14 +118,15 @@ static PyObject *rows_call(rows_fn fn, PyObject *const *a, Py_ssize_t n) {
     return PyLong_FromLong(st);
 }
 
-static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_append, a, n); }
-static PyObject *read_back(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_read, a, n); }
+static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_append, a, n, 0, 2); }
+static PyObject *read_back(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_read, a, n, 7, 0); }
 
 /* 10 addresses, 8 numbers, scale, causal, window, workspace and its size, the stream */
 static PyObject *fwd(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *p[10], *ws, *stream;
     int v[8], window, i;
     if (!count_is(n, 24)) return NULL;
+    if (!tensor_ok(a[0], 1) || !tensor_ok(a[8], 1) || !tensor_ok(a[1], 0)) return NULL;   /* q, o, the cache */
     for (i = 0; i < 10; ++i)
         if (!address(a[i], &p[i])) return NULL;
     for (i = 0; i < 8; ++i)
@@ -115,7 +152,9 @@ static PyObject *fwd(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *init(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *p[3];
     int i;
-    if (!count_is(n, 3)) return NULL;
+    if (!count_is(n, 4)) return NULL;
+    Py_INCREF(a[3]);
+    Py_XSETREF(g_current, a[3]);
     for (i = 0; i < 3; ++i)
         if (!address(a[i], &p[i])) return NULL;
     g_append = (rows_fn)p[0];
@@ -125,7 +164,7 @@ static PyObject *init(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 static PyMethodDef methods[] = {
-    {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, "init(fa_kv4_append, fa_kv4_read, fa_fwd_kv4): their addresses"},
+    {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, "init(fa_kv4_append, fa_kv4_read, fa_fwd_kv4, current_device): their addresses, and a function"},
     {"fa_kv4_append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "status of fa_kv4_append"},
     {"fa_kv4_read", (PyCFunction)(void (*)(void))read_back, METH_FASTCALL, "status of fa_kv4_read"},
     {"fa_fwd_kv4", (PyCFunction)(void (*)(void))fwd, METH_FASTCALL, "status of fa_fwd_kv4"},
@@ -136,5 +175,8 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "Argumen
 
 PyMODINIT_FUNC PyInit__fastcall(void) {
     g_data_ptr = PyUnicode_InternFromString("data_ptr");
-    return g_data_ptr == NULL ? NULL : PyModule_Create(&module);
+    g_get_device = PyUnicode_InternFromString("get_device");
+    g_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+    if (g_data_ptr == NULL || g_get_device == NULL || g_is_contiguous == NULL) return NULL;
+    return PyModule_Create(&module);
 }

@@ -11,12 +11,22 @@
 // movmatrix per 8 keys.  The order of channels along K is free in S (Q is permuted alike)
 // and so is the order of channels along M in O, so each thread takes contiguous bytes.
 //
-// The cache streams through a per-warp ring of 16-key tiles filled with 16-byte cp.async
+// The cache streams through a per-warp ring of 32-key tiles filled with 16-byte cp.async
 // copies (every wait is for the thread's own copies, so no barrier and nothing to time
 // out).  The work of all sequences and heads is one line of 128-key units cut into equal
 // shares, one per CTA: a long sequence is spread over many CTAs and many short ones share
 // a CTA, whatever the lengths.  A (sequence, head, row block) that ends up in several CTAs
 // is merged by the last of them to finish, from partial results in the workspace.
+//
+// What bounds it: a token and head is 144 bytes at d = 128, and at the rate at which memory
+// delivers them an SM has to take in 44 codes a cycle.  Dequantising 8 of them is 12
+// instructions of two issue cycles each, so the arithmetic, not the memory, is what a long
+// cache waits for: 4 x 32 heads on 16384 keys of 128 channels take 74 us, 4.1 TB/s, where the
+// copies alone take 57 and the arithmetic alone 72; without the FMAs of the dequantisation
+// 62, without all of it 48, without the MMAs 65.  Keeping 8, 12 or 16 warps to an SM (255,
+// 168, 128 registers) makes no difference.  A short call is a chain of latencies: lengths,
+// page, codes, a tile (0.8 us alone), the exchange, the arrival and the merge, 7.9 us for 8
+// heads on 700 keys.
 #pragma once
 
 #include <type_traits>
@@ -255,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     // tiles of the item, a step before the first of them is copied.  A run that is not there
     // (past the last visible key, or no page) is not copied, and masked.
     constexpr int kRuns = kOneRun ? 1 : 2;
-    const int32_t* l_table = p.pg.table == nullptr ? nullptr : p.pg.table + (long long)l_b * p.pg.max_pages;
     int l_page[kRuns], l_off[kRuns];             // of the lane's tile; page -1: not there
     uint32_t l_row[kRuns];                       // and its first row in the cache
     int l_at = 0, l_u = u0;                      // the next tile's lane, and the unit of lane 0
@@ -267,8 +276,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             const int pos = l_pos + lane * kUnit + 16 * i;
             l_page[i] = -1;
             if (pos < l_hi && l_u + lane < u1) {
-                const int n = page_div(p.pg, pos, l_off[i]);
-                l_page[i] = l_table != nullptr ? __ldg(l_table + n) : l_b * p.pg.max_pages + n;
+                l_page[i] = page_of(p.pg, l_b, page_div(p.pg, pos, l_off[i]));
             }
         }
     };
@@ -335,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     l_lo = y.lo + warp * kTile;
                     l_hi = y.hi;
                     l_b = y.b;
-                    if (l_table != nullptr) l_table = p.pg.table + (long long)l_b * p.pg.max_pages;
                 }
                 l_left = l_units;
                 l_pos = l_lo;
@@ -356,10 +363,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     constexpr int kMT = 4 * kVW;     // 16-channel tiles of O^T
     float acc[NB][kMT][4];
     float sumr[NB][4];               // sums of the rounded probabilities (every lane's copy is whole)
-    float sum[NB][2];                // this lane's share of the sums, not rounded
+    float2 sum[NB];                  // this lane's share of the sums, not rounded
     float ref[NB][2];                // reference max of rows 2t, 2t + 1 (log2 units), equal in all lanes of a t
     float top[NB][2];                // raw score above which the reference moves
-    float neg[NB][2];                // -ref, or 0 while the row has seen no key
+    float2 neg[NB];                  // -ref, or 0 while the row has seen no key
     uint8_t* const qs = smem + C::kQOff + lane * 16;
     // MMA row i of a 16-key tile (i < 8) is key i/2 + 4 (i mod 2), row 8 + i that key + 8
     const int key0 = (g >> 1) + 4 * (g & 1);
@@ -443,9 +450,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     if (m > ref[nb][c]) {
                         const float f = ex2_approx(ref[nb][c] - m);   // 0 from a reference of -inf
                         ref[nb][c] = m;
-                        neg[nb][c] = -m;
+                        (c == 0 ? neg[nb].x : neg[nb].y) = -m;
                         top[nb][c] = (m + 8.f) * inv_scale;
-                        sum[nb][c] *= f;
+                        (c == 0 ? sum[nb].x : sum[nb].y) *= f;
                         sumr[nb][c] *= f;
 #pragma unroll
                         for (int mt = 0; mt < kMT; ++mt) {
@@ -460,16 +467,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const float p0 = ex2_approx(fmaf(s[j][nb][0], p.scale_log2, neg[nb][0]));
-                const float p1 = ex2_approx(fmaf(s[j][nb][1], p.scale_log2, neg[nb][1]));
-                const float p2 = ex2_approx(fmaf(s[j][nb][2], p.scale_log2, neg[nb][0]));
-                const float p3 = ex2_approx(fmaf(s[j][nb][3], p.scale_log2, neg[nb][1]));
-                sum[nb][0] += p0 + p2;
-                sum[nb][1] += p1 + p3;
+                const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+                float2 e0 = __ffma2_rn(make_float2(s[j][nb][0], s[j][nb][1]), scale2, neg[nb]);
+                float2 e1 = __ffma2_rn(make_float2(s[j][nb][2], s[j][nb][3]), scale2, neg[nb]);
+                e0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+                e1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+                sum[nb] = __fadd2_rn(sum[nb], __fadd2_rn(e0, e1));
                 // P rounds to bf16 (2^-8) for the tensor cores; O is divided by the sum of
                 // the rounded values, so a row that one key dominates stays exact
-                pb[j][nb][0] = transpose8x8(pack_bf16x2(p0, p1));
-                pb[j][nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+                pb[j][nb][0] = transpose8x8(pack_bf16x2(e0.x, e0.y));
+                pb[j][nb][1] = transpose8x8(pack_bf16x2(e1.x, e1.y));
                 mma_bf16(sumr[nb], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, pb[j][nb][0], pb[j][nb][1]);
             }
         // ------------------------------------ O^T += V^T P^T
@@ -588,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             for (int c = 0; c < 4; ++c) sumr[nb][c] = 0.f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                sum[nb][c] = neg[nb][c] = 0.f;
                 ref[nb][c] = top[nb][c] = -INFINITY;
             }
+            sum[nb] = neg[nb] = make_float2(0.f, 0.f);
         }
         int pos = x.lo + seg_k * kUnit + warp * kTile;
         const int full_hi = x.all_hi - kTile;
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float l = sum[nb][c];
+                float l = c == 0 ? sum[nb].x : sum[nb].y;
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);

@@ -330,12 +330,16 @@ ATTEND = [
     (1, 1, 1, 1, 128, 256, 16, [4096], None, False, -1),              # one head over many CTAs
     (1, 1, 1, 3, 64, 4096, 1, [4001], None, True, 3000),              # one page, window over many CTAs
     (40, 2, 2, 1, 64, 16, 4, list(range(1, 41)), None, False, -1),    # many short sequences
-    (1, 1, 1, 128, 128, 32, 4, [128], None, True, -1),                # a whole prompt: one block of rows
-    (2, 2, 2, 129, 64, 64, 8, [129, 500], None, True, -1),            # a second block of one row
-    (2, 8, 2, 70, 128, 48, 10, [470, 60], [70, 33], True, 100),       # blocks that span heads; window; ragged
-    (1, 3, 1, 64, 128, 128, 3, [301], None, False, -1),               # no causal mask
+    (1, 1, 1, 128, 128, 32, 4, [128], None, True, -1),                # a whole prompt, few heads
     (1, 6, 2, 300, 64, 32, 40, [1111], None, True, 500),
-    (3, 4, 4, 200, 128, 16, 13, [200, 0, 7], [200, 0, 200], True, -1),
+    # many rows of many heads: the tensor-core tiles of 128 rows
+    (4, 8, 8, 160, 128, 32, 12, [160, 300, 0, 371], [160, 100, 160, 7], True, -1),
+    (4, 16, 8, 80, 64, 16, 30, [470, 80, 33, 200], None, True, 100),  # blocks that span heads; window
+    (2, 64, 16, 70, 128, 48, 10, [470, 60], [70, 33], True, -1),
+    (1, 32, 32, 200, 64, 64, 8, [201], None, False, -1),              # no causal mask
+    (1, 40, 8, 129, 128, 128, 6, [700], None, True, 333),
+    (1, 32, 32, 128, 128, 16, 8, [128], None, True, -1),              # whole prompts: one block of rows
+    (64, 2, 2, 130, 64, 16, 13, [(37 * b) % 209 for b in range(64)], None, True, -1),
 ]
 
 
@@ -346,68 +350,71 @@ def test_attention_matches_the_oracle(B, H, H_kv, N, d, page, maxp, key_lens, q_
     scale = float(np.float32(d ** -0.5))
     o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, q_lens, scale, causal, window)
     assert guards
-    check(c, bits, key_lens, q_lens, scale, causal, window, o, lse)
+    heads = None if B * H * N < 2000 else sorted({0, H // 2, H - 1})
+    check(c, bits, key_lens, q_lens, scale, causal, window, o, lse, heads=heads)
 
 
 @pytest.mark.parametrize("sigma,scale", [(4.0, 0.5), (0.05, 1.0), (1.0, 30.0), (2.0 ** -60, 1.0)])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("N", [2, 50])
-def test_attention_on_steep_and_flat_scores(sigma, scale, d, N):
+@pytest.mark.parametrize("H,H_kv,N", [(3, 1, 2), (3, 1, 50), (16, 16, 150)])
+def test_attention_on_steep_and_flat_scores(sigma, scale, d, H, H_kv, N):
     # steep: scores up to thousands, one key takes all; flat: every key counts alike
     key_lens = [700, 333]
-    c = filled(2, 1, 16, d, 44, key_lens, 31, sigma=sigma)
-    bits = normal_bf16((2, 3, N, d), 32, 0, min(sigma, 4.0))
+    c = filled(2, H_kv, 16, d, 44, key_lens, 31, sigma=sigma)
+    bits = normal_bf16((2, H, N, d), 32, 0, min(sigma, 4.0))
     o, lse, guards = run_kv4(c, to_device_bf16(bits), key_lens, None, scale, True, -1)
     assert guards
-    check(c, bits, key_lens, None, scale, True, -1, o, lse, what=f"sigma {sigma}")
+    check(c, bits, key_lens, None, scale, True, -1, o, lse, heads=None if H < 4 else [1], what=f"sigma {sigma}")
 
 
-@pytest.mark.parametrize("N", [1, 20])
-def test_scores_that_grow_along_the_keys(N):
+@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 20), (16, 65)])
+def test_scores_that_grow_along_the_keys(H_kv, N):
     # every tile moves the reference max: all the rescaling there is
     def edit(k, v):
         ramp = np.linspace(0.0, 6.0, k.shape[2])[None, None, :, None]
         k[:] = f32_to_bf16_bits((0.01 * bf16_bits_to_f32(k) + ramp).astype(np.float32))
-    c = filled(1, 2, 16, 128, 60, [960], 33, edit=edit)
-    bits = f32_to_bf16_bits(np.ones((1, 4, N, 128), np.float32))
+    c = filled(1, H_kv, 16, 128, 60, [960], 33, edit=edit)
+    bits = f32_to_bf16_bits(np.ones((1, 4 * H_kv, N, 128), np.float32))
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [960], None, 0.5, False, -1)
-    check(c, bits, [960], None, 0.5, False, -1, o, lse)
+    check(c, bits, [960], None, 0.5, False, -1, o, lse, heads=[0, 2 * H_kv + 1])
 
 
-@pytest.mark.parametrize("N,rows", [(3, 3), (12, 24), (40, 80), (150, 300)])
+@pytest.mark.parametrize("H_kv,N,rows", [(1, 3, 3), (1, 12, 24), (1, 40, 80), (32, 150, 150), (32, 100, 200)])
 @pytest.mark.parametrize("page", [16, 32])
-def test_what_a_query_does_not_see_has_no_influence(N, rows, page):
+def test_what_a_query_does_not_see_has_no_influence(H_kv, N, rows, page):
     # keys and values of the last tokens are NaN or infinite: the queries before them stay clean,
     # those that see them do not
     def edit(k, v):
         k[0, :, -2, 5] = 0x7FC0
         v[0, :, -1, 70] = 0x7F80
     key_lens = [200]
-    c = filled(1, 1, page, 128, 13, key_lens, 34, edit=edit)
-    bits = normal_bf16((1, rows // N, N, 128), 35, 0)
+    c = filled(1, H_kv, page, 128, 13, key_lens, 34, edit=edit)
+    bits = normal_bf16((1, H_kv * rows // N, N, 128), 35, 0)
+    heads = [0] if H_kv == 1 else [0, H_kv * rows // N - 1]
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, -1)
-    check(c, bits, key_lens, None, 0.09, True, -1, o, lse)
+    check(c, bits, key_lens, None, 0.09, True, -1, o, lse, heads=heads)
     import torch
     assert not torch.isnan(o[:, :, :N - 2].float()).any() and torch.isnan(o[:, :, N - 2:].float()).all()
     # behind a window too: an early poisoned value is out of sight of the last query
     def edit2(k, v):
         v[0, :, 190, 3] = 0xFF80
-    c = filled(1, 1, page, 128, 13, key_lens, 34, edit=edit2)
+    c = filled(1, H_kv, page, 128, 13, key_lens, 34, edit=edit2)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, 8)
-    check(c, bits, key_lens, None, 0.09, True, 8, o, lse)
+    check(c, bits, key_lens, None, 0.09, True, 8, o, lse, heads=heads)
 
 
-@pytest.mark.parametrize("N", [3, 30])
-def test_bad_pages_are_masked(N):
+@pytest.mark.parametrize("H_kv,N", [(2, 3), (2, 30), (32, 75)])
+def test_bad_pages_are_masked(H_kv, N):
     table = [[0, -1, 5, 2, 99, 1]]
-    c = filled(1, 2, 16, 64, 6, [90], 36, table=table)
-    bits = normal_bf16((1, 4, N, 64), 37, 0)
+    c = filled(1, H_kv, 16, 64, 6, [90], 36, table=table)
+    bits = normal_bf16((1, 2 * H_kv, N, 64), 37, 0)
+    heads = [0, 1, 2 * H_kv - 1]
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [90], None, 0.125, True, -1)
-    check(c, bits, [90], None, 0.125, True, -1, o, lse)
+    check(c, bits, [90], None, 0.125, True, -1, o, lse, heads=heads)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [5000], [2], 0.125, True, -1)     # length clamped to the pages
-    check(c, bits, [5000], [2], 0.125, True, -1, o, lse)
+    check(c, bits, [5000], [2], 0.125, True, -1, o, lse, heads=heads)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [-3], None, 0.125, False, -1)
-    check(c, bits, [-3], None, 0.125, False, -1, o, lse)
+    check(c, bits, [-3], None, 0.125, False, -1, o, lse, heads=heads)
 
 
 def test_a_cache_without_pages_is_empty():
@@ -474,12 +481,12 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(lse.cpu().numpy()[0, h] - rl) <= el)
 
 
-@pytest.mark.parametrize("N", [1, 5, 40])
-def test_results_are_the_same_bits_each_time_and_on_another_stream(N):
+@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 5), (16, 70)])
+def test_results_are_the_same_bits_each_time_and_on_another_stream(H_kv, N):
     import torch
     key_lens = [1900, 5, 777]
-    c = filled(3, 2, 16, 128, 120, key_lens, 51)
-    q = to_device_bf16(normal_bf16((3, 8, N, 128), 52, 0))
+    c = filled(3, H_kv, 16, 128, 120, key_lens, 51)
+    q = to_device_bf16(normal_bf16((3, 4 * H_kv, N, 128), 52, 0))
     o, lse, _ = run_kv4(c, q, key_lens, None, 0.09, True, -1)
     side = torch.cuda.Stream()
     for stream in (None, side, side.cuda_stream):
@@ -513,19 +520,20 @@ def test_a_decoding_loop_matches_the_dense_forward():
         assert np.abs(ld - lse.cpu().numpy()).max() <= 1e-4
 
 
-def test_captured_calls_replay_and_graphs_share_a_workspace():
+@pytest.mark.parametrize("H,H_kv", [(4, 1), (16, 16)])
+def test_captured_calls_replay_and_graphs_share_a_workspace(H, H_kv):
     import torch
     from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
-    B, H, H_kv, d, page, maxp = 2, 4, 1, 64, 16, 100
+    B, d, page, maxp = 2, 64, 16, 100
     c = Cache(B * maxp, H_kv, page, d, maxp, None)
     (k, v), _ = tokens(B, H_kv, 1500, d, 71)
     c.append(k, v, [1500, 1500])
     lens = ints([900, 1400])
     (k1, v1), _ = tokens(B, H_kv, 1, d, 72)
-    n = max(fa_fwd_kv4_workspace_size(B, H, H_kv, N, d) for N in (1, 5, 33))
+    n = max(fa_fwd_kv4_workspace_size(B, H, H_kv, N, d) for N in (1, 5, 140))
     ws = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
     graphs = []
-    for N in (1, 5, 33):
+    for N in (1, 5, 140):
         bits = normal_bf16((B, H, N, d), 73, 0)
         q = to_device_bf16(bits)
         o, lse = torch.empty_like(q), torch.empty((B, H, N), dtype=torch.float32, device="cuda")
@@ -548,7 +556,7 @@ def test_captured_calls_replay_and_graphs_share_a_workspace():
             graph.replay()
         torch.cuda.synchronize()
         for _, bits, o, lse, _ in graphs:
-            check(c, bits, new, None, 0.125, True, -1, o, lse, what=str(new))
+            check(c, bits, new, None, 0.125, True, -1, o, lse, heads=[0, H - 1], what=str(new))
 
 
 def test_workspace_contents_do_not_matter_and_nothing_past_it_is_touched():
@@ -566,3 +574,51 @@ def test_workspace_contents_do_not_matter_and_nothing_past_it_is_touched():
         if want is not None:
             assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
         want = (o, lse)
+
+
+def test_two_calls_at_once_and_one_workspace_for_unlike_shapes():
+    """Calls on two streams with a workspace each, and calls in turn on one workspace, whose parts
+    lie elsewhere for every shape."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4_workspace_size
+    shapes = [(3, 8, 1, 64, [1500, 40, 900]), (2, 2, 3, 128, [700, 1999]), (1, 4, 20, 128, [2000]), (2, 16, 70, 64, [300, 500])]
+    cases = []
+    for i, (B, H_kv, N, d, key_lens) in enumerate(shapes):
+        c = filled(B, H_kv, 32, d, 63, key_lens, 95 + i)
+        q = to_device_bf16(normal_bf16((B, 2 * H_kv, N, d), 96 + i, 0))
+        cases.append((c, q, key_lens, run_kv4(c, q, key_lens, None, 0.1, True, -1)))
+    n = max(fa_fwd_kv4_workspace_size(q.shape[0], q.shape[1], c.H_kv, q.shape[2], q.shape[3]) for c, q, _, _ in cases)
+    ws = torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda")
+    for c, q, key_lens, (o, lse, _) in cases + cases[::-1] + cases:
+        o2, lse2, _ = run_kv4(c, q, key_lens, None, 0.1, True, -1, workspace=ws)
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    from io_aware_exact_24_b200 import fa_fwd_kv4
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for turn in range(6):
+        for s, space in zip(streams, spaces):
+            c, q, key_lens, want = cases[(turn + (s is streams[0])) % len(cases)]
+            o, lse = torch.empty_like(q), torch.empty(q.shape[:3], dtype=torch.float32, device="cuda")
+            lens = ints(key_lens)
+            torch.cuda.current_stream().synchronize()
+            fa_fwd_kv4(q, *c.buffers, c.d_table, lens, None, o, lse, q.shape[0], q.shape[1], c.H_kv, q.shape[2], *c.sizes, 0.1,
+                       True, -1, space, n, s)
+            outs.append((o, lse, want, lens))
+    torch.cuda.synchronize()
+    for o, lse, want, _ in outs:
+        assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
+def test_lengths_below_zero_are_empty():
+    import torch
+    c = Cache(4, 2, 16, 64, 2, None)
+    (k, v), _ = tokens(2, 2, 5, 64, 97)
+    c.append(k, v, [3, 9], [-1, -7])
+    torch.cuda.synchronize()
+    assert torch.isnan(c.k_scales.float()).all()          # nothing was written
+    kb, vb = c.read([-1, -9], 4)
+    bits = normal_bf16((2, 2, 3, 64), 98, 0)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [-1, 0], [-5, 3], 0.1, True, -1)
+    assert (kb == 0).all() and (vb == 0).all() and (o == 0).all() and torch.isneginf(lse).all()

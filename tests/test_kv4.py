@@ -182,7 +182,8 @@ def test_arguments_become_the_same_call(lib):
     import ctypes
     import torch
     t = torch.zeros(64, dtype=torch.uint8)
-    assert append(k=t, key_lens=None, B=0) == append(k=t.data_ptr(), key_lens=None, B=0) == binding.FA_OK
+    # (the table is only taken as an address)
+    assert append(table=t, key_lens=None, B=0) == append(table=t.data_ptr(), key_lens=None, B=0) == binding.FA_OK
     for kw in ({}, dict(d=96), dict(ws_bytes=16), dict(q=P + 2), dict(N=0), dict(scale=-1), dict(window=7, causal=1, H=0)):
         a = dict(q=P, o=P, lse=P, kc=P, ks=P, vc=P, vs=P, table=P, key_lens=P, lens=P, B=1, H=2, H_kv=1, N=1, d=64,
                  num_pages=4, page_size=16, max_pages=4, scale=0.125, causal=0, window=-1, ws=P, ws_bytes=1 << 40) | kw
@@ -196,6 +197,36 @@ def test_arguments_become_the_same_call(lib):
         with pytest.raises((TypeError, OverflowError)):
             fwd(**bad)
     assert fwd(B=np.int64(0), scale=np.float32(0.5)) == binding.FA_OK
+
+
+def test_tensors_elsewhere_are_refused(lib):
+    import torch
+    t = torch.zeros(64, dtype=torch.uint8)
+    for call, kw in ((append, dict(k=t)), (append, dict(v=t)), (append, dict(kc=t)), (read, dict(k=t)), (read, dict(kc=t)),
+                     (fwd, dict(q=t)), (fwd, dict(o=t)), (fwd, dict(kc=t))):
+        with pytest.raises(ValueError, match="device"):
+            call(B=0, **kw)
+
+    class Elsewhere:                            # a tensor of another device, and one that is not contiguous
+        def __init__(self, device, contiguous):
+            self.device, self.contiguous = device, contiguous
+
+        def get_device(self):
+            return self.device
+
+        def is_contiguous(self):
+            return self.contiguous
+
+        def data_ptr(self):
+            return P
+
+    here = torch.cuda.current_device() if torch.cuda.is_available() else 0
+    for call, kw in ((append, "k"), (append, "v"), (read, "k"), (read, "v"), (fwd, "q"), (fwd, "o")):
+        assert call(B=0, **{kw: Elsewhere(here, True)}) == binding.FA_OK
+        with pytest.raises(ValueError, match="device"):
+            call(B=0, **{kw: Elsewhere(here + 1, True)})
+        with pytest.raises(ValueError, match="contiguous"):
+            call(B=0, **{kw: Elsewhere(here, False)})
 
 
 def test_workspace_size(lib):
