@@ -398,8 +398,9 @@ FA_API int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, v
  *   s = -m/8, rounded to 5 significant bits (ties to even),
  *   c = clamp(rint(x/s), -8, 7) + 8 (ties to even),  and c stands for (c - 8) * s,
  * which is exactly a bf16 number, |s|/2 from x at most, or 1.25 |s| next to -m, for which
- * there is no code (0.56 bytes an element instead of 2).  A group that holds a value that is not finite, or above 2^120 in
- * magnitude, stands for NaN; one whose values are all below 2^-107 stands for zeros.
+ * there is no code (0.56 bytes an element instead of 2).  A group that holds a value that
+ * is not finite, or above 2^120 in magnitude, stands for NaN; one whose values are all
+ * below 2^-107 stands for zeros.
  *
  * Sequences and pages:
  *   block_table  device int32 [B, max_pages]: the pages of each sequence in order; NULL:
@@ -411,7 +412,7 @@ FA_API int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, v
  *   key_lens     device int32 [B], required: tokens of each sequence INCLUDING those that
  *                the call appends or queries; clamped to [0, max_pages * page_size] by
  *                fa_kv4_read and fa_fwd_kv4.
- *   page_size    > 0, a multiple of 16; max_pages * page_size <= 2^30.
+ *   page_size    > 0, a multiple of 16; max_pages * page_size <= 2^30, and N_new, N <= 2^30.
  * Codes and scales are 16-byte aligned, k, v, q and o 16-byte, int32 arrays and lse 4-byte.
  * d is 64 or 128.  All calls are asynchronous on `stream` and run on the current device,
  * which must own the buffers; the library allocates nothing.

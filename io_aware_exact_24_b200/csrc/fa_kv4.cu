@@ -61,10 +61,10 @@ kv4::Paging paging(const int32_t* table, int num_pages, int page_size, int max_p
 }
 
 // Launch of the kernels that write and read tokens (see kv4::kRowsPerThread); false if B * H_kv
-// exceeds the launch limits.
+// exceeds the launch limits, or N that of positions.
 bool row_grid(int B, int H_kv, int N, int d, dim3* grid, bool* flat, uint32_t* rows) {
     const long long block = kv4::kRowThreads / (d / 8), per = block * kv4::kRowsPerThread, heads = (long long)B * H_kv;
-    if (heads > 0x7fffffffLL) return false;
+    if (heads > 0x7fffffffLL || N > kMaxPositions) return false;
     *flat = N < per && heads * N <= 0x7fffffffLL;
     *rows = *flat ? (uint32_t)(heads * N) : 0;
     *grid = *flat ? dim3((unsigned)((heads * N + block - 1) / block))
@@ -92,9 +92,9 @@ int row_block(long long R, long long heads) {
 int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
 
 // Whether the kernel for many rows (fa_kv4_rows.cuh) is the quicker one.  Per 128 keys it takes
-// about 1.6 us for each wave of its CTAs (128 rows each, one CTA per SM); the kernel for few rows
+// about 1.3 us for each wave of its CTAs (128 rows each, one CTA per SM); the kernel for few rows
 // takes 0.84 us of an SM for 16 rows, spread evenly.  Measured on both sides: 8 heads, 8192 keys,
-// 512 rows 103 and 95 us; 64 heads, 4096 keys, 64 rows 57 and 58 us, 128 rows 57 and 101 us.
+// 512 rows 87 and 95 us; 64 heads, 4096 keys, 64 rows 48 and 58 us, 128 rows 48 and 101 us.
 bool many_rows(long long R, long long heads, int num_sms) {
     const long long waves = ((R + 127) / 128 * heads + num_sms - 1) / num_sms;
     return R > 16 && 84 * ((R + 15) / 16) * heads > 130 * waves * num_sms;

@@ -167,10 +167,11 @@ __device__ __forceinline__ uint32_t minus_24(uint32_t s2) {
 // ---------------------------------------------------------------- writing the cache
 // Both kernels below give a thread 8 channels of a token.  With many tokens a head, block
 // (x, y) takes head x mod H_kv of sequence x / H_kv and steps through its tokens from block
-// y, four a thread, so that eight loads are on their way at once (2 x 32 x 8000 x 128 written
-// and read back: 188 -> 135 us against one token a thread).  Where a head has less than a
-// block's tokens, blocks take consecutive rows of all heads, one a thread (a decoding step's
-// tokens, 24 x 8 x 1 x 128: 6.0 -> 4.4 us).
+// y, four a thread, so that eight loads are on their way at once: 2 x 32 x 8000 x 128 written
+// and read back take 125 us (5.4 TB/s), with one token a thread 153, with two 128, with eight
+// 138 (8 x 12 x 1024 x 64: 13.4, 14.5, 13.1, 16.4).  Where a head has less than a block's
+// tokens, blocks take consecutive rows of all heads, one a thread (a decoding step's tokens,
+// 24 x 8 x 1 x 128: 6.0 -> 4.4 us, as first built).
 constexpr int kRowThreads = 256;
 constexpr int kRowsPerThread = 4;
 constexpr int kMaxRowBlocks = 65535;
@@ -209,38 +210,35 @@ __device__ __forceinline__ void quantise8(uint4 x, uint32_t& word, uint32_t& sca
     uint32_t e = max_nan_bf16x2(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
     e = max_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 1));
     e = max_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 2));
-    const float up = __uint_as_float(e << 16), down = __uint_as_float(e & 0xffff0000u);
-    const bool positive = up >= down;
+    const bool positive = __uint_as_float(e << 16) >= __uint_as_float(e & 0xffff0000u);
     const uint32_t mag = (positive ? e : e >> 16) & 0x7fffu;     // of a NaN: above kMagLargest
     // RNE of the 8-bit significand to 5 bits (a carry raises the exponent), over 8, sign turned
     const uint32_t five = (mag + 3u + ((mag >> 3) & 1u)) & ~7u;
-    const bool whole = mag <= kMagLargest, some = mag >= kMagSmallest;
-    scale = !whole ? kScaleNaN : (!some ? 0u : (five - (3u << 7)) | (positive ? 0x8000u : 0u));
+    scale = (five - (3u << 7)) | (positive ? 0x8000u : 0u);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(scale << 16)));
-    // rint(x / s), ties to even, without a division: x / s is k + 1/2 or at least 1/510 away
+    // rint(x / s), ties to even, without a division: x / s is k + 1/2 or at least 2^-9 away
     // from it (8-bit x, 5-bit s), so the product with an approximate 1 / s, rounded once to a
-    // grid of 2^-11 (6144 + .), lands on the tie exactly when the quotient does.  Four codes
-    // collect as the digits of a number in base 16, in the low bits of a float.
-    float w[2];
+    // grid of 2^-11 (6144 + .), lands on the tie exactly when the quotient does.  Then
+    // 1.5 * 2^23 + rint has the code less 8 in its lowest bits, and the sum of these times
+    // 16^i, modulo 2^32, is the word, less a constant.
+    constexpr uint32_t kMagic = 0x4B400000u;
+    word = 0x88888888u - kMagic * 0x11111111u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = 8388608.f + 8.f * 4369.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t b = xv[2 * h + (i >> 1)];
-            const float f = __uint_as_float((i & 1) ? (b & 0xffff0000u) : (b << 16));
-            const float q = fminf(__fmaf_rn(f, inv, 6144.f), 6144.f + 7.f);    // |x / s| <= 8.25: only 7 clamps
-            const float r = __fadd_rn(__fadd_rn(q, 12582912.f - 6144.f), -12582912.f);
-            w[h] = __fmaf_rn(r, (float)(1 << (4 * i)), w[h]);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const float f = __uint_as_float((i & 1) ? (xv[i >> 1] & 0xffff0000u) : (xv[i >> 1] << 16));
+        const float q = fminf(__fmaf_rn(f, inv, 6144.f), 6144.f + 7.f);    // |x / s| <= 8.25: only 7 clamps
+        word += __float_as_uint(__fadd_rn(q, 12582912.f - 6144.f)) << (4 * i);
     }
-    word = __byte_perm(__float_as_uint(w[0]), __float_as_uint(w[1]), 0x5410);
-    if (!whole || !some) word = 0x88888888u;
+    if (mag - kMagSmallest > kMagLargest - kMagSmallest) {
+        scale = mag > kMagLargest ? kScaleNaN : 0u;
+        word = 0x88888888u;
+    }
 }
 
-// Bound by memory: 4 D bytes read and 9 D / 8 written a token and head; the arithmetic is
-// about ten cycles a value and scheduler, two thirds of what the memory leaves.
+// 4 D bytes read and 9 D / 8 written a token and head, with the arithmetic close behind: of 2 x
+// 32 x 8000 x 128's 70 us (52 at the copy rate), where the scheduler issued in 79 of 100
+// cycles at 83 us, cheaper sums for the codes and 32-bit indexes took 13 away.
 template <int D, bool kFlat>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams p) {
     after_previous();
@@ -258,26 +256,24 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
     }
     const int b = bh / p.H_kv, h = bh - b * p.H_kv;
     const int nl = clamped(p.new_lens, b, p.N);
-    const long long first = (long long)__ldg(p.key_lens + b) - nl;
-    const long long top = (long long)p.pg.max_pages * p.pg.page_size;
+    const int first = max(0, __ldg(p.key_lens + b)) - nl;    // of the new tokens' positions
+    const uint32_t top = (uint32_t)(p.pg.max_pages * p.pg.page_size);
     const uint4* const k = p.k + (long long)bh * p.N * kLanes + sub;
     const uint4* const v = p.v + (long long)bh * p.N * kLanes + sub;
     // (a flat block's threads make one step each, together: they share the scales by shuffles)
-    for (long long n0 = (long long)blockIdx.y * (kRows * kEach); kFlat ? n0 == 0 : n0 < nl;
-         n0 += kFlat ? 1 : (long long)gridDim.y * (kRows * kEach)) {
+    for (int n0 = blockIdx.y * (kRows * kEach); kFlat ? n0 == 0 : n0 < nl; n0 += kFlat ? 1 : (int)gridDim.y * (kRows * kEach)) {
         uint4 kx[kEach], vx[kEach];
         uint32_t row[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const long long n = n0 + i * kRows + r, pos = first + n;
-            const bool in = valid && n < nl && pos >= 0 && pos < top;
+            const int n = n0 + i * kRows + r, pos = first + n;
             row[i] = 0xffffffffu;
             kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-            if (in) {
-                kx[i] = __ldg(k + n * kLanes);
-                vx[i] = __ldg(v + n * kLanes);
+            if (valid && n < nl && (uint32_t)pos < top) {
+                kx[i] = __ldg(k + (size_t)n * kLanes);
+                vx[i] = __ldg(v + (size_t)n * kLanes);
                 int off;
-                const int page = page_of(p.pg, b, page_div(p.pg, (int)pos, off));
+                const int page = page_of(p.pg, b, page_div(p.pg, pos, off));
                 if (page >= 0) row[i] = ((uint32_t)page * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size + (uint32_t)off;
             }
         }
@@ -320,7 +316,8 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t scale) {
                       __byte_perm(c, d, 0x7632));
 }
 
-// Bound by memory: 9 D / 8 bytes read and 4 D written a token and head.
+// Bound by memory: 9 D / 8 bytes read and 4 D written a token and head (2 x 32 x 8000 x 128: 56
+// us, 6.0 TB/s).
 template <int D, bool kFlat>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
     after_previous();
@@ -341,14 +338,15 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
     const long long first = p.first != nullptr ? (long long)__ldg(p.first + b) : 0;
     uint4* const k = p.k + (long long)bh * p.N * kLanes + sub;
     uint4* const v = p.v + (long long)bh * p.N * kLanes + sub;
-    for (long long n0 = (long long)blockIdx.y * (kRows * kEach); n0 < p.N && valid; n0 += kFlat ? p.N : (long long)gridDim.y * (kRows * kEach)) {
+    for (int n0 = blockIdx.y * (kRows * kEach); n0 < p.N && valid; n0 += kFlat ? p.N : (int)gridDim.y * (kRows * kEach)) {
         uint32_t kw[kEach], vw[kEach], ks[kEach], vs[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const long long pos = first + n0 + i * kRows + r;
+            const int n = n0 + i * kRows + r;
+            const long long pos = first + n;
             kw[i] = vw[i] = 0x88888888u;
             ks[i] = vs[i] = 0;
-            if (n0 + i * kRows + r < p.N && pos >= 0 && pos < kl) {
+            if (n < p.N && pos >= 0 && pos < kl) {
                 int off;
                 const int page = page_of(p.pg, b, page_div(p.pg, (int)pos, off));
                 if (page >= 0) {
@@ -362,10 +360,10 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const long long n = n0 + i * kRows + r;
+            const int n = n0 + i * kRows + r;
             if (n >= p.N) continue;
-            k[n * kLanes] = dequantise8(kw[i], ks[i]);
-            v[n * kLanes] = dequantise8(vw[i], vs[i]);
+            k[(size_t)n * kLanes] = dequantise8(kw[i], ks[i]);
+            v[(size_t)n * kLanes] = dequantise8(vw[i], vs[i]);
         }
     }
 }

@@ -136,7 +136,8 @@ SHARED = [
     (dict(table=P + 2), MISALIGNED), (dict(key_lens=P + 1), MISALIGNED), (dict(lens=P + 3), MISALIGNED),
 ]
 TOKENS = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=P + 8), MISALIGNED), (dict(v=P + 2), MISALIGNED),
-          (dict(H_kv=65536), UNSUPPORTED), (dict(B=65535, H_kv=65535), UNSUPPORTED)]
+          (dict(H_kv=65536), UNSUPPORTED), (dict(B=65535, H_kv=65535), UNSUPPORTED),
+          (dict(N=(1 << 30) + 1), UNSUPPORTED)]
 FWD = [
     (dict(H=3, H_kv=2), INVALID), (dict(H=-2), INVALID), (dict(H=65536), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=-1.0), INVALID),
