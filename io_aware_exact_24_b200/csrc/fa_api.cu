@@ -613,8 +613,14 @@ int launch_rows(const CUtensorMap& tq, const CUtensorMap& to, const fa::kv4::Row
         set[dev] = cudaFuncSetAttribute(fa::kv4::rows_kernel<D, kOneRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (set[dev] != cudaSuccess) return ::cuda_fail("cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", set[dev]);
-    const dim3 grid((unsigned)((p.rows.R + fa::kBlockM - 1) / fa::kBlockM), (unsigned)p.H_kv, (unsigned)B);
+    const unsigned blocks = (unsigned)p.row_blocks;
+    const dim3 grid(blocks * (unsigned)p.splits, (unsigned)p.H_kv, (unsigned)B);
     e = launch_overlapped(fa::kv4::rows_kernel<D, kOneRun>, grid, fa::kv4::kRowsThreads, smem, stream, tq, to, p);
+    if (e == cudaSuccess && p.splits > 1) {
+        const fa::kv4::JoinParams j{reinterpret_cast<const float4*>(p.part), p.part_ml, p.o, p.lse, p.rows.R, p.splits};
+        e = launch_overlapped(fa::kv4::join_kernel<D>, dim3(D / 8 * (fa::kBlockM / 32), blocks, (unsigned)(B * p.H_kv)),
+                              fa::kv4::kJoinWarps * 32, 0, stream, j);
+    }
     return e == cudaSuccess ? FA_OK : ::cuda_fail("kernel launch (4-bit cache attention, many rows)", e);
 }
 }  // namespace
@@ -626,6 +632,8 @@ int launch_kv4_rows(const void* q, void* o, int B, int d, fa::kv4::RowsParams p,
         return FA_ERR_CUDA;
     }
     p.wait_limit = kWaitLimitCycles;
+    p.row_blocks = (p.rows.R + fa::kBlockM - 1) / fa::kBlockM;
+    p.split_inv = (65535 + p.splits) / p.splits;
     const bool one = p.pg.page_size % 32 == 0;
     if (d == 64) return one ? launch_rows<64, true>(tq, to, p, B, stream) : launch_rows<64, false>(tq, to, p, B, stream);
     return one ? launch_rows<128, true>(tq, to, p, B, stream) : launch_rows<128, false>(tq, to, p, B, stream);

@@ -91,18 +91,42 @@ int row_block(long long R, long long heads) {
 }
 int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
 
-// Whether the kernel for many rows (fa_kv4_rows.cuh) is the quicker one.  Per 128 keys it takes
-// about 1.3 us for each wave of its CTAs (128 rows each, one CTA per SM); the kernel for few rows
-// takes 0.84 us of an SM for 16 rows, spread evenly.  Measured on both sides: 8 heads, 8192 keys,
-// 512 rows 87 and 95 us; 64 heads, 4096 keys, 64 rows 48 and 58 us, 128 rows 48 and 101 us.
-bool many_rows(long long R, long long heads, int num_sms) {
-    const long long waves = ((R + 127) / 128 * heads + num_sms - 1) / num_sms;
-    return R > 16 && 84 * ((R + 15) / 16) * heads > 130 * waves * num_sms;
+// CTAs of the kernel for many rows (fa_kv4_rows.cuh) that share the keys of a block of rows,
+// where the blocks alone would leave half the SMs idle: at most as many as fill the SMs once,
+// each with two tiles or more of the longest sequence there could be.  8 heads of 32768 keys,
+// 128 rows: one CTA a block about 340 us, 18 of them 32; 1024 rows, two CTAs, 173.
+int most_splits(long long R, long long heads, int num_sms) {
+    return (int)std::max<long long>(1, num_sms / ((R + 127) / 128 * heads));
+}
+int key_splits(long long R, long long heads, int num_sms, long long keys) {
+    return (int)std::max<long long>(1, std::min<long long>(most_splits(R, heads, num_sms), keys / 256));
 }
 
-// Workspace of the attention: two partial results per CTA, then the arrival words.
+// Whether the kernel for many rows is the quicker one, for sequences of up to `keys` keys.  Each
+// wave of its CTAs takes about 3 us and 1.3 for each tile of 128 keys; the kernel for few rows
+// 0.65 us of an SM for 8 rows and 128 keys, or 0.84 for 16, evenly spread, and 0.1 us for each
+// part that it merges.  Measured, in us, many rows and few:
+//     8 heads,   700 keys     20 rows 11.3,  9.8     64 rows 11.9, 10.5     256 rows 13.7,  16.5
+//     8 heads,  8192 keys     20 rows 16.6, 19.8     64 rows 17.0, 28.8    1024 rows 56.8, 173
+//    64 heads,  4096 keys     20 rows 34.5, 38.3     64 rows 34.6, 57.7     256 rows 50.7, 184
+//    64 heads, window 2048    20 rows 25.3, 27.1     64 rows 26.8, 40.0     256 rows 31.9, 117
+//   512 heads,   700 keys (d = 64)   20 rows 49.7, 37.9     64 rows 49.6, 73.6
+bool many_rows(long long R, long long heads, int splits, int num_sms, long long keys) {
+    if (R <= 16) return false;
+    const long long tiles = (keys + 127) / 128, waves = ((R + 127) / 128 * heads * splits + num_sms - 1) / num_sms;
+    const double many = (splits > 1 ? 7. : 5.) + (double)waves * (3. + 1.3 * (double)((tiles + splits - 1) / splits));
+    const int rb = row_block(R, heads);
+    const long long items = (R + rb - 1) / rb * heads;
+    const long long parts = std::min<long long>(tiles, std::max<long long>(1, (long long)num_sms * ctas_per_sm(rb) / items));
+    const double few = (rb == 8 ? 9. : 12.5) + (rb == 8 ? .65 : .84) * (double)items * (double)keys / 128. / num_sms +
+                       .1 * (double)std::min<long long>(parts, 50);
+    return many < few;
+}
+
+// Workspace of the attention: two partial results per CTA, then the arrival words.  The kernel
+// for many rows keeps one partial result per CTA where it splits the keys.
 struct Layout {
-    size_t part, ml, words, total;
+    size_t part, ml, words, group_words, rows_ml, total;
 };
 Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
     const long long R = (long long)(H / H_kv) * N_q;
@@ -113,37 +137,52 @@ Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
     L.part = 0;
     L.ml = round_up(slots * rb * d * 4);
     L.words = L.ml + round_up(slots * rb * 16);
-    L.total = L.words + round_up((size_t)std::min<long long>(entries, kv4::kMaxEntries) * H_kv * 8);
+    L.group_words = L.words + round_up((size_t)std::min<long long>(entries, kv4::kMaxEntries) * H_kv * 8);
+    L.total = L.group_words + round_up(slots * 8);
+    const int splits = R > 16 ? most_splits(R, (long long)B * H_kv, num_sms) : 1;
+    if (splits > 1) {
+        const size_t parts = (size_t)splits * B * H_kv * ((R + 127) / 128) * 128;   // rows
+        L.rows_ml = round_up(parts * d * 4);
+        L.total = std::max(L.total, L.rows_ml + round_up(parts * 12));
+    }
     return L;
 }
 
 std::once_flag g_once[64];
 int g_status[64];
 
-template <int D, int NB>
+template <int D, int NB, bool kGroups>
 cudaError_t set_smem() {
     const int bytes = kv4::Cfg<D, NB>::kSmemBytes;
     const cudaError_t e =
-        cudaFuncSetAttribute(kv4::attend_kernel<D, NB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncSetAttribute(kv4::attend_kernel<D, NB, false, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(kv4::attend_kernel<D, NB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return cudaFuncSetAttribute(kv4::attend_kernel<D, NB, true, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 int prepare_attend(int dev) {
     std::call_once(g_once[dev], [&] {
-        cudaError_t e = set_smem<64, 1>();
-        if (e == cudaSuccess) e = set_smem<64, 2>();
-        if (e == cudaSuccess) e = set_smem<128, 1>();
-        if (e == cudaSuccess) e = set_smem<128, 2>();
+        cudaError_t e = set_smem<64, 1, false>();
+        if (e == cudaSuccess) e = set_smem<64, 1, true>();
+        if (e == cudaSuccess) e = set_smem<64, 2, false>();
+        if (e == cudaSuccess) e = set_smem<128, 1, false>();
+        if (e == cudaSuccess) e = set_smem<128, 1, true>();
+        if (e == cudaSuccess) e = set_smem<128, 2, false>();
         g_status[dev] = e == cudaSuccess ? FA_OK : cuda_fail("cudaFuncSetAttribute(MaxDynamicSharedMemorySize)", e);
     });
     return g_status[dev];
 }
 
-template <int D, int NB>
+template <int D, int NB, bool kGroups>
 cudaError_t launch_attend(const kv4::AttendParams& p, int num_sms, cudaStream_t s) {
     const int grid = num_sms * ctas_per_sm(8 * NB), smem = kv4::Cfg<D, NB>::kSmemBytes;
-    return launch_overlapped(p.pg.page_size % kv4::kTile == 0 ? kv4::attend_kernel<D, NB, true> : kv4::attend_kernel<D, NB, false>,
+    return launch_overlapped(p.pg.page_size % kv4::kTile == 0 ? kv4::attend_kernel<D, NB, true, kGroups>
+                                                              : kv4::attend_kernel<D, NB, false, kGroups>,
                              grid, kv4::kThreads, smem, s, p);
+}
+template <int D>
+cudaError_t launch_attend(const kv4::AttendParams& p, int rb, bool groups, int num_sms, cudaStream_t s) {
+    if (rb != 8) return launch_attend<D, 2, false>(p, num_sms, s);
+    return groups ? launch_attend<D, 1, true>(p, num_sms, s) : launch_attend<D, 1, false>(p, num_sms, s);
 }
 
 }  // namespace
@@ -259,7 +298,11 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     rows.window = window_left < 0 ? -1 : std::min(window_left, kMaxPositions);
     const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (many_rows(R, (long long)B * H_kv, sms)) {
+    long long keys = (long long)max_pages * page_size;
+    if (window_left >= 0) keys = std::min(keys, (long long)rows.window + N_q);
+    const int splits = key_splits(R, (long long)B * H_kv, sms, keys);
+    if (many_rows(R, (long long)B * H_kv, splits, sms, keys)) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
         kv4::RowsParams p{};
         p.k_codes = static_cast<const uint8_t*>(k_codes);
         p.k_scales = static_cast<const uint16_t*>(k_scales);
@@ -268,8 +311,12 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
         p.pg = pg;
         p.rows = rows;
         p.H_kv = H_kv;
+        p.o = static_cast<__nv_bfloat16*>(o);
         p.lse = lse;
         p.scale_log2 = scale_log2;
+        p.splits = splits;
+        p.part = reinterpret_cast<float*>(ws);
+        p.part_ml = reinterpret_cast<float*>(ws + L.rows_ml);
         return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
     }
     const int rb = row_block(R, (long long)B * H_kv);
@@ -290,6 +337,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     p.part = reinterpret_cast<float*>(ws + L.part);
     p.part_ml = reinterpret_cast<float*>(ws + L.ml);
     p.words = reinterpret_cast<unsigned long long*>(ws + L.words);
+    p.group_words = reinterpret_cast<unsigned long long*>(ws + L.group_words);
     const long long entries = (long long)B * p.row_blocks;
     // the line of units of one launch stays within int
     const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
@@ -298,8 +346,11 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
         p.rb0 = (int)(e0 % p.row_blocks);
         p.E = (int)std::min(chunk, entries - e0);
         p.ticket = next_ticket();
-        const cudaError_t e = d == 64 ? (rb == 8 ? launch_attend<64, 1>(p, sms, s) : launch_attend<64, 2>(p, sms, s))
-                                      : (rb == 8 ? launch_attend<128, 1>(p, sms, s) : launch_attend<128, 2>(p, sms, s));
+        // parts of an item, if the sequences are alike
+        const long long parts = std::min<long long>((keys + kv4::kUnit - 1) / kv4::kUnit, (long long)sms * ctas_per_sm(rb) / (p.E * H_kv));
+        const int nr = (int)std::min<long long>(R, rb);
+        const bool groups = parts > kv4::kFlat * (d == 64 ? kv4::row_groups<64>(nr) : kv4::row_groups<128>(nr));
+        const cudaError_t e = d == 64 ? launch_attend<64>(p, rb, groups, sms, s) : launch_attend<128>(p, rb, groups, sms, s);
         if (e != cudaSuccess) return cuda_fail("kernel launch (4-bit cache attention)", e);
     }
     return FA_OK;

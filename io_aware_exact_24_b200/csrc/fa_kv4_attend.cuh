@@ -41,6 +41,16 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp and step: two MMA tiles
 constexpr int kUnit = kTile * kWarps;            // keys per CTA and step
 constexpr int kMaxEntries = 512;                 // (sequence, row block) pairs per launch
+// Merging an item costs its last CTA 0.1 us for each part that a thread has to add, so where
+// these can be more than kFlat, every kFan are merged by the last of theirs and then these sums
+// (kGroups: 2 x 4 heads on 40000 keys, 222 parts, 48 -> 18.8 us; 8 x 4 on 8192, 55 parts, 17.4 ->
+// 14.3).  Elsewhere it would cost 0.6 to 1.5 us a call.
+constexpr int kFan = 16, kFlat = 36;
+// Threads that share the parts of a row of an item of nr rows.
+template <int D>
+__host__ __device__ constexpr int row_groups(int nr) {
+    return 2 * nr * (D / 4) > kThreads ? 1 : kThreads / (nr * (D / 4));
+}
 
 struct AttendParams {
     const __nv_bfloat16* q;    // [B, H_kv, R, D]
@@ -60,6 +70,7 @@ struct AttendParams {
     float* part;               // per CTA two partial results: [2][RB][D] sums and [2][RB][4] (max, sums)
     float* part_ml;
     unsigned long long* words; // arrival words [E, H_kv]
+    unsigned long long* group_words;   // and one per partial result
     unsigned long long ticket; // not 0
 };
 
@@ -159,7 +170,7 @@ __device__ __forceinline__ Entry entry_of(const AttendParams& p, int e) {
     return entry_of_rows<RB, kTile, kUnit>(p.rows, p.pg, b, g * RB);
 }
 
-template <int D, int NB, bool kOneRun>
+template <int D, int NB, bool kOneRun, bool kGroups>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kernel(const AttendParams p) {
     using C = Cfg<D, NB>;
     constexpr int RB = C::kRB;
@@ -558,13 +569,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         }
     };
 
+    // The CTAs [cf, cl] that share an item, and this one's group of them [gf, ge].
+    struct Sharers {
+        int cf, cl, gf, ge, first_slot;
+        bool grouped;
+        // a CTA whose share starts inside the item has it first, else last: all but cf have it first
+        __device__ __forceinline__ int slot_of(int c) const { return c == cf ? first_slot : 2 * c; }
+    };
+    auto sharers = [&](int first, int units, int nr) {
+        int ea = each;
+        asm volatile("" : "+r"(ea));             // (worked out twice, not kept over the tiles)
+        auto holder = [&](int v) {               // the CTA whose share has unit v
+            const int big = more * (ea + 1);
+            return v < big ? v / (ea + 1) : more + (v - big) / ea;
+        };
+        Sharers s;
+        s.cf = holder(first);
+        s.cl = holder(first + units - 1);
+        s.gf = s.cf + ((int)blockIdx.x - s.cf) / kFan * kFan;
+        s.ge = min(s.gf + kFan - 1, s.cl);
+        s.first_slot = 2 * s.cf + (ea * s.cf + min(s.cf, more) >= first ? 0 : 1);
+        s.grouped = kGroups && s.cl - s.cf >= kFlat * row_groups<D>(nr);
+        return s;
+    };
     for (int u = u0; u < u1;) {
         // ============================================ a segment: units seg_k .. of an item
         const int n = min(x.units - seg_k, u1 - u);
         const int item_first = pre[seg_e] + seg_h * x.units;
         const bool whole = seg_k == 0 && n == x.units;
         unsigned long long* const word = p.words + (long long)seg_e * p.H_kv + seg_h;
-        unsigned long long found = 0;
+        unsigned long long found = 0, gfound = 0;
         if (!whole && tid == 0) found = arrive_claim(word, p.ticket);
         {
             // Q as B fragments, two k-steps of the MMA to 16 bytes, shared by the warps
@@ -585,6 +619,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             row_hi[tid] = hi;
         }
         __syncthreads();
+        if (kGroups && !whole && tid == 0) {
+            const Sharers sh = sharers(item_first, x.units, x.nr);
+            if (sh.grouped) gfound = arrive_claim(p.group_words + sh.slot_of(sh.gf), p.ticket);
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -695,25 +733,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
         if constexpr (NB > 1) combine(std::integral_constant<int, 1>{});
         if (!whole) {
             // ---------------------------------------- partial: the last CTA of the item merges
-            auto holder = [&](int v) {           // the CTA whose share has unit v
-                const int big = more * (each + 1);
-                return v < big ? v / (each + 1) : more + (v - big) / each;
-            };
-            const int cf = holder(item_first), cl = holder(item_first + x.units - 1);
-            __syncthreads();
-            if (tid == 0) misc[0] = arrive_last(word, found, p.ticket, cl - cf + 1) ? 1 : 0;
-            __syncthreads();
-            if (misc[0]) {
-                // a CTA whose share starts inside the item has it first, else last: all but
-                // the first CTA have it first
-                const long long first = (long long)(2 * cf + (share(cf) >= item_first ? 0 : 1)) * RB;
-                auto at = [&](int c) { return c == cf ? first : (long long)(2 * c) * RB; };
+            const Sharers sh = sharers(item_first, x.units, nr);
+            for (bool last_level = !kGroups || !sh.grouped;; last_level = true) {
+                __syncthreads();
+                // parts 0 .. c1: the CTAs from base on, or every kFan-th
+                const int apart = kGroups && last_level && sh.grouped ? kFan : 1;
+                const int base = last_level ? sh.cf : sh.gf, c1 = ((last_level ? sh.cl : sh.ge) - base) / apart;
+                if (tid == 0)
+                    misc[0] = arrive_last(last_level ? word : p.group_words + sh.slot_of(base), last_level ? found : gfound,
+                                          p.ticket, c1 + 1);
+                __syncthreads();
+                if (!misc[0]) break;
+                auto at = [&](int c) { return (long long)sh.slot_of(base + c * apart) * RB; };
                 // sums, 4 channels a thread: of up to kEach rows, or, with few rows, of some of the
                 // CTAs of one row.  kAhead * kEach loads at a time, the first of them on their way
                 // while the rows' statistics are made.
                 const int items = nr * (D / 4);
-                const int groups = items * 2 > kThreads ? 1 : kThreads / items;
-                constexpr int kEach = RB * (D / 4) / kThreads, kAhead = NB == 1 ? 2 : 4;
+                const int groups = row_groups<D>(nr);
+                constexpr int kEach = RB * (D / 4) / kThreads, kAhead = 4;
                 static_assert(kEach * kThreads == RB * (D / 4), "rows of a block");
                 float mc[kAhead][kEach];
                 float4 y[kAhead][kEach];
@@ -728,21 +765,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                         for (int e = 0; e < kEach; ++e) {
                             // (without branches, so that the loads go out together)
                             const int c = one ? c0 + i : c0 + (i * kEach + e) * groups;
-                            const long long r = at(min(c, cl)) + min(row_of(e), nr - 1);
+                            const long long r = at(min(c, c1)) + min(row_of(e), nr - 1);
                             mc[i][e] = __ldcg(p.part_ml + r * 4);
                             y[i][e] = __ldcg(reinterpret_cast<const float4*>(p.part + r * D) + c40);
-                            if (c > cl) mc[i][e] = -INFINITY;
+                            if (c > c1) mc[i][e] = -INFINITY;
                         }
                 };
                 float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);       // the warp's first row, a CTA per lane
-                if (warp < nr && cf + lane <= cl) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(cf + lane) + warp) * 4));
-                fetch(cf + gi);
+                if (warp < nr && lane <= c1) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(lane) + warp) * 4));
+                fetch(gi);
                 // statistics of each row: a warp per row, a lane per CTA
-                float* const fin = st_max;       // [RB] merged max, [RB] 1 / merged sum (the warps' own are used up)
+                float* const fin = st_max;       // [RB] merged max, then 1 / merged sum, or both sums (the warps' own are used up)
                 for (int rr = warp; rr < nr; rr += kWarps) {
                     float m = -INFINITY, lr = 0.f, l = 0.f;
-                    for (int c = cf + lane; c <= cl; c += 32) {
-                        if (rr != warp || c != cf + lane) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(c) + rr) * 4));
+                    for (int c = lane; c <= c1; c += 32) {
+                        if (rr != warp || c != lane) ml = __ldcg(reinterpret_cast<const float4*>(p.part_ml + (at(c) + rr) * 4));
                         const float n = fmaxf(m, ml.x);
                         const float f = m == -INFINITY ? 0.f : ex2_approx(m - n);
                         const float h = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - n);
@@ -763,12 +800,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     }
                     if (lane == 0) {
                         fin[rr] = n;
-                        fin[RB + rr] = l == 0.f ? 0.f : 1.f / lr;
-                        p.lse[row0 + rr] = l == 0.f ? -INFINITY : (n + log2f(l)) * 0.69314718055994531f;
+                        if (last_level) {
+                            fin[RB + rr] = l == 0.f ? 0.f : 1.f / lr;
+                            p.lse[row0 + rr] = l == 0.f ? -INFINITY : (n + log2f(l)) * 0.69314718055994531f;
+                        } else {
+                            fin[RB + rr] = lr;
+                            fin[2 * RB + rr] = l;
+                        }
                     }
                 }
                 __syncthreads();
+                if (!last_level && tid < nr)     // into the first part's place, which all have read
+                    *reinterpret_cast<float4*>(p.part_ml + (at(0) + tid) * 4) = make_float4(fin[tid], fin[RB + tid], fin[2 * RB + tid], 0.f);
                 auto put = [&](int rr, int c4, const float4& a) {
+                    if (!last_level) {
+                        *reinterpret_cast<float4*>(p.part + (at(0) + rr) * D + 4 * c4) = a;
+                        return;
+                    }
                     const float inv = fin[RB + rr];
                     uint2 pk;
                     pk.x = pack_bf16x2(a.x * inv, a.y * inv);
@@ -778,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                 float4 a[kEach];
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c = cf + gi; c <= cl;) {
+                for (int c = gi; c <= c1;) {
 #pragma unroll
                     for (int e = 0; e < kEach; ++e) {
                         const float m = fin[min(row_of(e), RB - 1)];
@@ -792,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                         }
                     }
                     c += step;
-                    if (c <= cl) fetch(c);
+                    if (c <= c1) fetch(c);
                 }
                 if (!one) {
 #pragma unroll
@@ -815,6 +863,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                         put(row_of(0), c40, v);
                     }
                 }
+                if (last_level) break;
             }
         }
         __syncthreads();                         // statistics, exchange buffer and row limits are free again

@@ -141,9 +141,15 @@ struct RowsParams {
     Paging pg;
     Rows rows;
     int H_kv;
+    __nv_bfloat16* o;                // [B, H_kv, R, D]
     float* lse;                      // [B, H_kv, R]
     float scale_log2;
     unsigned long long wait_limit;
+    int row_blocks;                  // of kBlockM rows
+    int splits;                      // ranges of keys of a block of rows, one CTA each
+    int split_inv;                   // ceil(2^16 / splits)
+    float* part;                     // with splits > 1, per CTA: sums of P V [D/4][128 rows][4],
+    float* part_ml;                  // and per row the max, the sum of rounded P and of P: [3][128]
 };
 
 // ---------------------------------------------------------------- codes to bf16

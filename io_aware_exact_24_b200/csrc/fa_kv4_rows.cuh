@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     auto bar_p_full = [&](int b) { return bar(5 + 2 * F::kStages + b); };
     auto bar_pv_done = [&](int b) { return bar(5 + C::kPBufs + 2 * F::kStages + b); };
     const uint32_t bar_drain = bar(5 + 2 * C::kPBufs + 2 * F::kStages);
+    volatile uint32_t* const part_at = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kMiscOff + 8);
     uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + C::kMiscOff);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
     const uint32_t mref_w = base + C::kMrefOff;
@@ -117,7 +118,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // rows that see more keys (causal: the later ones of a head) start first
-    const int m0 = (int)(gridDim.x - 1 - blockIdx.x) * kBlockM;
+    int back = (int)blockIdx.x, split = 0;
+    if (p.splits > 1) {          // CTAs are few then: x * ceil(2^16 / splits) >> 16 is exact
+        back = (int)((blockIdx.x * (uint32_t)p.split_inv) >> 16);
+        split = (int)blockIdx.x - back * p.splits;
+    }
+    const int m0 = (p.row_blocks - 1 - back) * kBlockM;
     const int h = blockIdx.y, b = blockIdx.z;
 
     // ---- setup
@@ -155,8 +161,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     fence_proxy_async_smem();
     after_previous();
-    const Entry x = entry_of_rows<kBlockM, 32, kBlockN>(p.rows, p.pg, b, m0);
-    const int n_kv = x.hi > x.lo ? x.units : 0;
+    Entry x = entry_of_rows<kBlockM, 32, kBlockN>(p.rows, p.pg, b, m0);
+    int n_kv = x.hi > x.lo ? x.units : 0;
+    if (p.splits > 1) {
+        const int t0 = (int)((uint32_t)n_kv * (uint32_t)split / (uint32_t)p.splits);
+        n_kv = (int)((uint32_t)n_kv * (uint32_t)(split + 1) / (uint32_t)p.splits) - t0;
+        x.lo += t0 * kBlockN;
+    }
+    if (threadIdx.x == 0) {      // (kept here: registers are short)
+        part_at[0] = ((uint32_t)(b * p.H_kv + h) * (uint32_t)p.row_blocks + (uint32_t)(m0 / kBlockM)) * (uint32_t)p.splits + (uint32_t)split;
+        part_at[1] = (uint32_t)m0;
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
@@ -184,7 +199,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 for (int i = 0; i < kRuns; ++i) {
                     const int pos = x.lo + (j + lane) * kBlockN + w * 32 + 16 * i;
                     l_row[i] = 0xffffffffu;
-                    if (j + lane < n_kv && pos < x.hi) {
+                    if (pos < x.kl) {
                         int off;
                         const int page = page_of(p.pg, b, page_div(p.pg, pos, off));
                         if (page >= 0)
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             if (lane == 0 && n_kv > 0) {
                 mbar_arrive_expect_tx(bar_q_full, (uint32_t)F::kTileBytes);
                 for (int bx = 0; bx < F::kBoxes; ++bx)
-                    tma_load_4d(q_tile + bx * F::kBoxBytes, &tm_q, bar_q_full, bx * F::kBoxCols, m0, h, b, policy_evict_first());
+                    tma_load_4d(q_tile + bx * F::kBoxBytes, &tm_q, bar_q_full, bx * F::kBoxCols, (int)part_at[1], h, b, policy_evict_first());
                 (void)wait_own_work(bar_q_full, 0);   // the copy has landed before the CTA can exit
             }
         } else if (warp == kMmaWarp || warp == kPvWarp) {
@@ -398,13 +413,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int qd = warp & 3, g = warp >> 2;
         const int r = qd * 32 + lane;
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
-        const int row = m0 + r;
         int lo, lim;
-        row_keys(p.rows, x.kl, x.ql, row, lo, lim);
-        if (row >= p.rows.R) lo = 0, lim = 0x7fffffff;   // no row: nothing of it is kept, and it asks for no mask
+        row_keys(p.rows, x.kl, x.ql, m0 + r, lo, lim);
         const float c = p.scale_log2;
         float m_seen = -INFINITY, lu = 0.f;
         uint32_t nan_groups = 0;         // groups of V that a key this row sees holds as NaN
+        constexpr uint32_t kNone = 1u << 31;
+        if (lim <= lo) {                 // no row, or no key: nothing of it is kept, and it asks for no mask
+            lo = 0, lim = 0x7fffffff;
+            nan_groups = kNone;
+        }
         bool ok = true;
         if (n_kv > 0 && 32 * g < D / 2) {
             // Q into TMEM, in the order of the codes: columns 32g .. 32g + 31 of this row
@@ -539,36 +557,76 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             good = __all_sync(0xffffffffu, wait_bounded(bar_drain, 0, abort_flag, p.wait_limit));
             if (good) tc_fence_after();
         }
+        const int row = (int)part_at[1] + r;
         epi[g * kBlockM + r] = m_seen;
         epi[(2 + g) * kBlockM + r] = lu;
         epi[(4 + g) * kBlockM + r] = __uint_as_float(nan_groups);
         good = !named_bar_or(kBarQuadBase + qd, 64, !good);
+        nan_groups = __float_as_uint(epi[4 * kBlockM + r]) | __float_as_uint(epi[5 * kBlockM + r]);
+        const bool none = nan_groups & kNone;
         const float m0w = epi[r], m1w = epi[kBlockM + r];
-        const float m_fin = fmaxf(m0w, m1w);
+        const float m_fin = none ? -INFINITY : fmaxf(m0w, m1w);
         const float f0 = (m0w == m_fin) ? 1.f : ex2_approx(m0w - m_fin);
         const float f1 = (m1w == m_fin) ? 1.f : ex2_approx(m1w - m_fin);
-        const float lu_row = epi[2 * kBlockM + r] * f0 + epi[3 * kBlockM + r] * f1;
-        nan_groups = __float_as_uint(epi[4 * kBlockM + r]) | __float_as_uint(epi[5 * kBlockM + r]);
-        if (good) {
+        const float lu_row = none ? 0.f : epi[2 * kBlockM + r] * f0 + epi[3 * kBlockM + r] * f1;
+        if (good && p.splits > 1) {
+            const size_t at = part_at[0];
+            if (row < p.rows.R && g == 0) {
+                float* const ml = p.part_ml + at * 3 * kBlockM + r;
+                ml[0] = m_fin;
+                ml[2 * kBlockM] = lu_row;
+            }
+            if (have_o) {
+                uint32_t u[32];
+                tmem_ld32(tmem + lane_off + C::kColL, u);
+                tmem_wait_ld();
+                reg_after_wait(u[0]);
+                if (row < p.rows.R && g == 0) p.part_ml[(at * 3 + 1) * kBlockM + r] = __uint_as_float(u[0]);
+#pragma unroll
+                for (int q4 = 0; q4 < D / 64; ++q4) {
+                    const int col0 = g * (D / 2) + 32 * q4;
+                    const bool is_nan = (nan_groups >> (col0 / kGroup)) & 1u;
+                    tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)col0, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        reg_after_wait(u[i]);
+                        if (is_nan) u[i] = 0x7fc00000u;
+                    }
+                    uint4* const dst = reinterpret_cast<uint4*>(p.part) + (at * (D / 4) + col0 / 4) * kBlockM + r;
+                    if (row < p.rows.R)
+#pragma unroll
+                        for (int v4 = 0; v4 < 8; ++v4) {   // channels back in order
+                            const int u0 = 8 * (v4 / 2) + v4 % 2;
+                            dst[v4 * kBlockM] = make_uint4(u[u0], u[u0 + 2], u[u0 + 4], u[u0 + 6]);
+                        }
+                }
+            } else if (row < p.rows.R && g == 0) {
+                p.part_ml[(at * 3 + 1) * kBlockM + r] = 0.f;
+            }
+        } else if (good) {
             float l_row = 0.f;
             if (have_o) {
                 uint32_t u[32];
                 tmem_ld32(tmem + lane_off + C::kColL, u);
                 tmem_wait_ld();
                 reg_after_wait(u[0]);
-                l_row = __uint_as_float(u[0]);
+                l_row = none ? 0.f : __uint_as_float(u[0]);
             }
             const float inv_row = l_row == 0.f ? 0.f : 1.f / l_row;
 #pragma unroll
             for (int q4 = 0; q4 < D / 64; ++q4) {
                 const int col0 = g * (D / 2) + 32 * q4;
-                const float inv_l = ((nan_groups >> (col0 / kGroup)) & 1u) ? __int_as_float(0x7fc00000) : inv_row;
+                const float inv_l = !none && ((nan_groups >> (col0 / kGroup)) & 1u) ? __int_as_float(0x7fc00000) : inv_row;
                 uint32_t u[32];
                 if (have_o) {
                     tmem_ld32(tmem + lane_off + C::kColO + (uint32_t)col0, u);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) reg_after_wait(u[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        reg_after_wait(u[i]);
+                        if (none) u[i] = 0u;
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) u[i] = 0u;
@@ -588,8 +646,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         fence_proxy_async_smem();
         const bool any_bad = named_bar_or(kBarSoftmaxAll, kSoftmaxWarps * 32, !good);
-        if (!any_bad && threadIdx.x == 0) {
-            for (int bx = 0; bx < F::kOBoxes; ++bx) tma_store_4d(&tm_o, q_tile + bx * kSwizzleBoxBytes, bx * 64, m0, h, b);
+        if (!any_bad && threadIdx.x == 0 && p.splits == 1) {
+            for (int bx = 0; bx < F::kOBoxes; ++bx) tma_store_4d(&tm_o, q_tile + bx * kSwizzleBoxBytes, bx * 64, (int)part_at[1], h, b);
             bulk_commit_group();
             bulk_wait_group_read0();
         }
@@ -601,6 +659,89 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// Joins the ranges of a block of rows.  Block (x, y, z): 32 rows and 8 channels of row block y
+// of head z, a row per lane, the ranges dealt out to the warps.  The parts are in L2, so what
+// counts is that all loads are on their way at once.
+constexpr int kJoinWarps = 4;
+
+struct JoinParams {
+    const float4* part;
+    const float* part_ml;
+    __nv_bfloat16* o;
+    float* lse;
+    int R, splits;
+};
+
+struct Joined {
+    float m = -INFINITY, l = 0.f, lu = 0.f;   // reference max, sums of rounded P and of P
+    float acc[8] = {};
+    // A part without a key the row sees counts nothing, whatever its sums hold.
+    __device__ __forceinline__ void add(float m2, float l2, float lu2, const float (&v)[8]) {
+        const bool none = m2 == -INFINITY && lu2 == 0.f;
+        const float top = fmaxf(m, m2);
+        const float a = m == top ? 1.f : ex2_approx(m - top), w = m2 == top ? 1.f : ex2_approx(m2 - top);
+        m = top;
+        l = l * a + (none ? 0.f : l2 * w);
+        lu = lu * a + (none ? 0.f : lu2 * w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = acc[i] * a + (none ? 0.f : v[i] * w);
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams p) {
+    after_previous();
+    __shared__ float other[kJoinWarps - 1][11][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c8 = blockIdx.x % (D / 8), r0 = (int)(blockIdx.x / (D / 8)) * 32;
+    const int row = (int)blockIdx.y * kBlockM + r0 + lane;
+    if (row - lane >= p.R) return;
+    const int r = r0 + min(lane, p.R - 1 - (row - lane));   // behind the last row nothing was written
+    const size_t at = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * p.splits;
+    Joined x;
+    constexpr int kEach = 4;
+    for (int s0 = warp; s0 < p.splits; s0 += kJoinWarps * kEach) {
+        float ml[kEach][3], v[kEach][8];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const size_t a = at + min(s0 + i * kJoinWarps, p.splits - 1);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) ml[i][k] = p.part_ml[(a * 3 + k) * kBlockM + r];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 f = p.part[(a * (D / 4) + 2 * c8 + k) * kBlockM + r];
+                v[i][4 * k] = f.x, v[i][4 * k + 1] = f.y, v[i][4 * k + 2] = f.z, v[i][4 * k + 3] = f.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (s0 + i * kJoinWarps < p.splits) x.add(ml[i][0], ml[i][1], ml[i][2], v[i]);
+    }
+    if (warp > 0) {
+        float(*const to)[32] = other[warp - 1];
+        to[0][lane] = x.m, to[1][lane] = x.l, to[2][lane] = x.lu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[3 + i][lane] = x.acc[i];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps - 1; ++w) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = other[w][3 + i][lane];
+        x.add(other[w][0][lane], other[w][1][lane], other[w][2][lane], v);
+    }
+    if (row >= p.R) return;
+    const size_t out = (size_t)blockIdx.z * p.R + row;
+    const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+    uint4 y;
+    y.x = pack_bf16x2(x.acc[0] * inv, x.acc[1] * inv), y.y = pack_bf16x2(x.acc[2] * inv, x.acc[3] * inv);
+    y.z = pack_bf16x2(x.acc[4] * inv, x.acc[5] * inv), y.w = pack_bf16x2(x.acc[6] * inv, x.acc[7] * inv);
+    *reinterpret_cast<uint4*>(p.o + out * D + 8 * c8) = y;
+    if (c8 == 0) p.lse[out] = x.lu == 0.f ? -INFINITY : (x.m + log2f(x.lu)) * 0.69314718055994531f;
 }
 
 }  // namespace kv4

@@ -340,6 +340,17 @@ ATTEND = [
     (1, 40, 8, 129, 128, 128, 6, [700], None, True, 333),
     (1, 32, 32, 128, 128, 16, 8, [128], None, True, -1),              # whole prompts: one block of rows
     (64, 2, 2, 130, 64, 16, 13, [(37 * b) % 209 for b in range(64)], None, True, -1),
+    # long keys of few heads: an item over many CTAs, merged in two levels
+    (1, 8, 1, 1, 128, 32, 200, [6111], None, True, -1),
+    (1, 3, 1, 1, 64, 16, 300, [4001], None, False, -1),
+    (2, 13, 1, 1, 128, 16, 300, [4799, 3300], None, True, 4000),
+    (3, 4, 2, 2, 64, 64, 60, [3833, 0, 3500], [2, 1, 1], True, -1),
+    # many rows of few heads: the keys of a block in ranges, then joined
+    (1, 8, 1, 5, 128, 32, 200, [6111], None, True, -1),
+    (2, 4, 2, 33, 64, 16, 300, [4800, 129], [33, 20], True, -1),
+    (3, 4, 2, 24, 128, 48, 70, [3300, 0, 50], None, False, -1),       # ranges without a key
+    (1, 10, 5, 140, 64, 64, 40, [2222], [131], True, 700),            # ranges that windows leave out
+    (1, 1, 1, 300, 128, 16, 160, [2500], None, True, -1),
 ]
 
 
@@ -379,7 +390,7 @@ def test_scores_that_grow_along_the_keys(H_kv, N):
     check(c, bits, [960], None, 0.5, False, -1, o, lse, heads=[0, 2 * H_kv + 1])
 
 
-@pytest.mark.parametrize("H_kv,N,rows", [(1, 3, 3), (1, 12, 24), (1, 40, 80), (32, 150, 150), (32, 100, 200)])
+@pytest.mark.parametrize("H_kv,N,rows", [(1, 3, 3), (1, 12, 24), (1, 40, 80), (32, 150, 150), (32, 100, 200), (4, 150, 300)])
 @pytest.mark.parametrize("page", [16, 32])
 def test_what_a_query_does_not_see_has_no_influence(H_kv, N, rows, page):
     # keys and values of the last tokens are NaN or infinite: the queries before them stay clean,
@@ -401,6 +412,29 @@ def test_what_a_query_does_not_see_has_no_influence(H_kv, N, rows, page):
     c = filled(1, H_kv, page, 128, 13, key_lens, 34, edit=edit2)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, 8)
     check(c, bits, key_lens, None, 0.09, True, 8, o, lse, heads=heads)
+
+
+@pytest.mark.parametrize("H,N", [(2, 1), (2, 3), (8, 30)])       # merged parts; ranges of keys
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32)])
+def test_poisoned_keys_and_missing_pages_of_a_long_sequence(H, N, d, page):
+    import torch
+    def edit(k, v):
+        k[0, :, -2, 5] = 0x7FC0
+        v[0, :, -1, 40] = 0x7F80
+    n = 5950
+    pages = 6016 // page
+    table = np.random.default_rng(39).permutation(pages)[None]
+    c = filled(1, 1, page, d, pages, [n], 39, table=table, edit=edit)
+    bits = normal_bf16((1, H, N, d), 40, 0)
+    o, lse, _ = run_kv4(c, to_device_bf16(bits), [n], None, 0.09, True, -1)
+    check(c, bits, [n], None, 0.09, True, -1, o, lse, heads=[0, H - 1])
+    assert not torch.isnan(o[:, :, :max(0, N - 2)].float()).any() and torch.isnan(o[:, :, max(0, N - 2):].float()).any()
+    table[0, pages // 5:pages // 2] = -1         # ranges without a page
+    c.table[...] = table
+    c.d_table.copy_(ints(table))
+    for lens, window in (([n - 2], -1), ([n - 2], 3300), ([pages // 2 * page], 40)):
+        o, lse, _ = run_kv4(c, to_device_bf16(bits), lens, None, 0.09, True, window)
+        check(c, bits, lens, None, 0.09, True, window, o, lse, heads=[0, H - 1], what=str((lens, window)))
 
 
 @pytest.mark.parametrize("H_kv,N", [(2, 3), (2, 30), (32, 75)])
@@ -481,7 +515,7 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(lse.cpu().numpy()[0, h] - rl) <= el)
 
 
-@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 5), (16, 70)])
+@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 5), (2, 40), (16, 70)])
 def test_results_are_the_same_bits_each_time_and_on_another_stream(H_kv, N):
     import torch
     key_lens = [1900, 5, 777]
@@ -559,13 +593,47 @@ def test_captured_calls_replay_and_graphs_share_a_workspace(H, H_kv):
             check(c, bits, new, None, 0.125, True, -1, o, lse, heads=[0, H - 1], what=str(new))
 
 
-def test_workspace_contents_do_not_matter_and_nothing_past_it_is_touched():
+def test_long_sequences_of_few_heads_in_graphs_that_share_a_workspace():
+    """Items over many CTAs, merged in two levels, and ranges of keys that are joined, as the
+    sequence grows and shrinks under the captured calls."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size
+    H, d, page, maxp = 8, 128, 32, 200
+    c = filled(1, 1, page, d, maxp, [6400], 74)
+    lens = ints([6400])
+    n = max(fa_fwd_kv4_workspace_size(1, H, 1, N, d) for N in (1, 2, 4, 30))
+    ws = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for N in (1, 2, 4, 30):
+        bits = normal_bf16((1, H, N, d), 75, 0)
+        q = to_device_bf16(bits)
+        o, lse = torch.empty_like(q), torch.empty((1, H, N), dtype=torch.float32, device="cuda")
+
+        def step():
+            fa_fwd_kv4(q, *c.buffers, c.d_table, lens, None, o, lse, 1, H, 1, N, *c.sizes, 0.0625, True, -1, ws, n)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        graphs.append((graph, bits, o, lse, q))
+    for new in ([6400], [17], [6001], [6001], [0], [1290], [6399]):
+        lens.copy_(ints(new))
+        for graph, *_ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, bits, o, lse, _ in graphs:
+            check(c, bits, new, None, 0.0625, True, -1, o, lse, heads=[0, H - 1], what=str(new))
+
+
+@pytest.mark.parametrize("H,N,keys", [(2, 8, 3000), (8, 1, 6000), (3, 20, 6000), (1, 150, 5000)])
+def test_workspace_contents_do_not_matter_and_nothing_past_it_is_touched(H, N, keys):
     import torch
     from io_aware_exact_24_b200 import fa_fwd_kv4_workspace_size
-    key_lens = [3000]
-    c = filled(1, 1, 64, 128, 50, key_lens, 91)
-    q = to_device_bf16(normal_bf16((1, 2, 8, 128), 92, 0))
-    n = fa_fwd_kv4_workspace_size(1, 2, 1, 8, 128)
+    key_lens = [keys]
+    c = filled(1, 1, 64, 128, 100, key_lens, 91)
+    q = to_device_bf16(normal_bf16((1, H, N, 128), 92, 0))
+    n = fa_fwd_kv4_workspace_size(1, H, 1, N, 128)
     want = None
     for fill in (0, 0xFF, 0x7F):
         buf = torch.full((n + 512,), fill, dtype=torch.uint8, device="cuda")
