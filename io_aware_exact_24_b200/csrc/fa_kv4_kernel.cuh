@@ -242,9 +242,9 @@ __device__ __forceinline__ void quantise8(uint4 x, uint32_t& word, uint32_t& sca
     }
 }
 
-// 4 D bytes read and 9 D / 8 written a token and head, with the arithmetic close behind: of 2 x
-// 32 x 8000 x 128's 70 us (52 at the copy rate), where the scheduler issued in 79 of 100
-// cycles at 83 us, cheaper sums for the codes and 32-bit indexes took 13 away.
+// 4 D bytes read and 9 D / 8 written a token and head, with the arithmetic close behind: 2 x 32 x
+// 8000 x 128 take 70 us, 52 at the copy rate, and the schedulers issue in 76 of 100 cycles
+// (before the codes were summed as integers, and with 64-bit indexes, 83 us).
 template <int D, bool kFlat>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams p) {
     after_previous();

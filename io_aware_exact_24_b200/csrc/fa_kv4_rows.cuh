@@ -4,18 +4,30 @@
 // The rows of a key/value head (fa_kv4_kernel.cuh: Rows) come in blocks of 128, one CTA each.
 // The kernel is the forward of fa_fwd_kernel.cuh (S = Q K^T and O += P V in TMEM, two softmax
 // warps per lane quadrant, the reference max that moves by 2^8) with another source of K and
-// V: four warps read the codes of a 128-key tile into registers, one tile ahead, turn them
+// V: four warps copy the codes of a 128-key tile to shared memory, one tile ahead, turn them
 // into bf16 and store them to the swizzled tiles that the MMAs read.  The values are exact
 // (fa_kv4_kernel.cuh), so the tensor cores multiply what a read-back cache would hold, and no
 // bf16 copy of the cache passes through memory.
 //
 // The codes of a 32-bit word come out as channels (0,4) (1,5) (2,6) (3,7).  K is stored in
-// that order, Q goes to TMEM in it, and of O, whose columns follow V's, the
-// epilogue picks the columns back.
+// that order, Q goes to TMEM in it, and of O, whose columns follow V's, the epilogue picks the
+// columns back.
+//
+// Where the blocks are few, CTAs share one's keys in ranges and leave unnormalised sums in the
+// workspace; join_kernel, a launch behind, adds them up.  It has a block for every 32 rows and 8
+// channels, where the last CTA of a block of rows, alone, would take 0.1 us or more for each range.
 //
 // A NaN group of V would reach the rows that do not see its key as 0 * NaN: it is stored as
 // zeros and noted in a mask per tile, and the softmax threads, which know what their row sees,
 // make the group's channels NaN at the end.
+//
+// What bounds it: 2 x 32 heads (8 of keys), 512 queries, 8000 keys take 172 us, 756 TFLOP/s;
+// the products alone are 78 us at the rate of a large one.  256 blocks are 1.73 waves, so the
+// SMs are idle for 14 % of it.  Else no unit is full (tensor pipe 43 % of the cycles, ALU 44,
+// exponentials 42, issue 54): a tile takes a CTA 1.25 us, in which the makers turn 32768 codes
+// into 64 KB of operands, the eight softmax warps take 128 x 128 scores, and each waits for the
+// other, since shared memory and TMEM hold two tiles.  A short call is launch, setup, tiles,
+// epilogue and join: 8 x 128 rows on 700 keys, 12.5 us.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"

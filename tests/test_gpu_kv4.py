@@ -451,10 +451,11 @@ def test_bad_pages_are_masked(H_kv, N):
     check(c, bits, [-3], None, 0.125, False, -1, o, lse, heads=heads)
 
 
-def test_a_cache_without_pages_is_empty():
+@pytest.mark.parametrize("N", [3, 300])
+def test_a_cache_without_pages_is_empty(N):
     import torch
     from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
-    B, H, H_kv, N, d = 2, 4, 2, 3, 64
+    B, H, H_kv, d = 2, 4, 2, 64
     (k, v), _ = tokens(B, H_kv, N, d, 38)
     lens, none = ints([3, 3]), (None,) * 4
     for table, maxp in ((None, 0), (None, 4), (ints([[0] * 4] * B), 4)):
