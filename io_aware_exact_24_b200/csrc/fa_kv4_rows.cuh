@@ -581,14 +581,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const float f0 = (m0w == m_fin) ? 1.f : ex2_approx(m0w - m_fin);
         const float f1 = (m1w == m_fin) ? 1.f : ex2_approx(m1w - m_fin);
         const float lu_row = none ? 0.f : epi[2 * kBlockM + r] * f0 + epi[3 * kBlockM + r] * f1;
-        if (good && p.splits > 1) {
+        if (p.splits > 1) {
+            // (a part that a wait gave up on is an empty one, so that no old contents are joined)
             const size_t at = part_at[0];
             if (row < p.rows.R && g == 0) {
                 float* const ml = p.part_ml + at * 3 * kBlockM + r;
-                ml[0] = m_fin;
-                ml[2 * kBlockM] = lu_row;
+                ml[0] = good ? m_fin : -INFINITY;
+                ml[2 * kBlockM] = good ? lu_row : 0.f;
             }
-            if (have_o) {
+            if (good && have_o) {
                 uint32_t u[32];
                 tmem_ld32(tmem + lane_off + C::kColL, u);
                 tmem_wait_ld();
