@@ -59,6 +59,25 @@ def test_values_are_bf16_numbers_and_near():
     assert np.array_equal(kv4.unpack(kv4.pack(codes)), codes)
 
 
+def test_a_product_with_a_near_reciprocal_rounds_as_the_quotient():
+    # what the kernels rely on: an 8-bit over a 5-bit significand is k + 1/2 or at least 2^-9 from
+    # it, so x * (1/s), with 1/s off by an ulp or two, on a grid of 2^-11, ties where x / s does
+    x, s, e = np.meshgrid(np.arange(128, 256), np.arange(16, 32), np.arange(-9, 1), indexing="ij")
+    x = x * 2.0 ** e
+    quotient = x / s
+    keep = quotient <= 8.25
+    off = np.abs(quotient - np.floor(quotient) - 0.5)[keep]
+    assert off[off > 0].min() == 2.0 ** -9
+    near = (1.0 / s).astype(np.float32)
+    for steps in (-2, -1, 0, 1, 2):
+        inv = near.copy()
+        for _ in range(abs(steps)):
+            inv = np.nextafter(inv, np.float32(np.sign(steps) * 4), dtype=np.float32)
+        for sign in (1, -1):
+            on_grid = np.rint((6144.0 + sign * x * inv.astype(np.float64)) * 2048.0) / 2048.0
+            assert np.array_equal(np.rint(on_grid - 6144.0)[keep], np.rint(sign * quotient)[keep])
+
+
 @pytest.mark.parametrize("bad,want", [(np.nan, "nan"), (np.inf, "nan"), (-np.inf, "nan"), (2.0 ** 121, "nan"),
                                       (2.0 ** -108, "zero"), (2.0 ** 120, "value"), (2.0 ** -107, "value")])
 def test_ends_of_the_range(bad, want):
