@@ -81,15 +81,26 @@ unsigned long long next_ticket() {
     return t;
 }
 
-// Rows per block.  One MMA column block holds 8 query rows; two share a dequantised operand,
-// at 0.84 us of an SM for 128 keys where one takes 0.6, but leave two CTAs to an SM instead of
-// three.  So 8 where a second block of 16 would be half empty (20 rows of 64 heads within a
-// window of 2048: 27 and 33 us; 4096 keys: 37 and 36), and where there is little work, when
-// latency counts (16 rows of 8 heads, 8192 keys: 19 and 25 us; of 64 heads, 4096: 29 and 28).
-int row_block(long long R, long long heads) {
-    return R <= 8 || (R > 16 && R <= 24) || (R <= 64 && heads * ((R + 15) / 16) <= 32) ? 8 : 16;
-}
 int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
+
+// Time of the kernel for few rows, in us, for sequences of up to `keys` keys and rb rows a block.
+// One MMA column block holds 8 query rows: 0.62 us of an SM for 128 keys; two share a
+// dequantised operand, at 0.84, but leave two CTAs to an SM instead of three and start later.
+// Each part of an item adds to its merge, of 8 rows up to two levels' (fa_kv4_attend.cuh).
+double few_rows_us(long long R, long long heads, int rb, long long keys, int num_sms) {
+    const long long items = (R + rb - 1) / rb * heads;
+    const double units = (double)items * (double)keys / kv4::kUnit;
+    const double parts = std::min((double)keys / kv4::kUnit, (double)num_sms * ctas_per_sm(rb) / (double)items);
+    return rb == 8 ? 9. + .62 * units / num_sms + std::min(5., .1 * parts) : 12.5 + .84 * units / num_sms + .2 * parts;
+}
+
+// Rows per block, 8 or 16: the quicker one.  Measured, in us, 8 and 16 (16 rows):
+//      8 heads    700 keys  9.8, 12.9     8192 keys 19.4, 25.1     65536 keys 48.2, 46.1
+//     64 heads    700 keys 12.8, 15.3     2048 keys 21.3, 23.6      4096 keys 30.6, 29.7
+//     16 heads  32768 keys 47.2, 41.5;  2 heads, 131072 keys 33.6, 55.9
+int row_block(long long R, long long heads, long long keys, int num_sms) {
+    return R <= 8 || few_rows_us(R, heads, 8, keys, num_sms) <= few_rows_us(R, heads, 16, keys, num_sms) ? 8 : 16;
+}
 
 // CTAs of the kernel for many rows (fa_kv4_rows.cuh) that share the keys of a block of rows,
 // where the blocks alone would leave half the SMs idle: at most as many as fill the SMs once,
@@ -102,10 +113,8 @@ int key_splits(long long R, long long heads, int num_sms, long long keys) {
     return (int)std::max<long long>(1, std::min<long long>(most_splits(R, heads, num_sms), keys / 256));
 }
 
-// Whether the kernel for many rows is the quicker one, for sequences of up to `keys` keys.  Each
-// wave of its CTAs takes about 3 us and 1.3 for each tile of 128 keys; the kernel for few rows
-// 0.65 us of an SM for 8 rows and 128 keys, or 0.84 for 16, evenly spread, and 0.1 us for each
-// part that it merges.  Measured, in us, many rows and few:
+// Whether the kernel for many rows is the quicker one: each wave of its CTAs takes about 3 us and
+// 1.3 for each tile of 128 keys.  Measured, in us, many rows and few:
 //     8 heads,   700 keys     20 rows 11.3,  9.8     64 rows 11.9, 10.5     256 rows 13.7,  16.5
 //     8 heads,  8192 keys     20 rows 16.6, 19.8     64 rows 17.0, 28.8    1024 rows 56.8, 173
 //    64 heads,  4096 keys     20 rows 34.5, 38.3     64 rows 34.6, 57.7     256 rows 50.7, 184
@@ -115,11 +124,7 @@ bool many_rows(long long R, long long heads, int splits, int num_sms, long long 
     if (R <= 16) return false;
     const long long tiles = (keys + 127) / 128, waves = ((R + 127) / 128 * heads * splits + num_sms - 1) / num_sms;
     const double many = (splits > 1 ? 7. : 5.) + (double)waves * (3. + 1.3 * (double)((tiles + splits - 1) / splits));
-    const int rb = row_block(R, heads);
-    const long long items = (R + rb - 1) / rb * heads;
-    const long long parts = std::min<long long>(tiles, std::max<long long>(1, (long long)num_sms * ctas_per_sm(rb) / items));
-    const double few = (rb == 8 ? 9. : 12.5) + (rb == 8 ? .65 : .84) * (double)items * (double)keys / 128. / num_sms +
-                       .1 * (double)std::min<long long>(parts, 50);
+    const double few = few_rows_us(R, heads, row_block(R, heads, keys, num_sms), keys, num_sms);
     return many < few;
 }
 
@@ -128,9 +133,8 @@ bool many_rows(long long R, long long heads, int splits, int num_sms, long long 
 struct Layout {
     size_t part, ml, words, group_words, rows_ml, total;
 };
-Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
+Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms, int rb) {
     const long long R = (long long)(H / H_kv) * N_q;
-    const int rb = row_block(R, (long long)B * H_kv);
     const size_t slots = 2 * (size_t)num_sms * ctas_per_sm(rb);
     const long long entries = (R + rb - 1) / rb * B;
     Layout L{};
@@ -146,6 +150,11 @@ Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms) {
         L.total = std::max(L.total, L.rows_ml + round_up(parts * 12));
     }
     return L;
+}
+
+// Whatever the lengths that choose rb.
+size_t workspace_size(int B, int H, int H_kv, int N_q, int d, int num_sms) {
+    return std::max(layout(B, H, H_kv, N_q, d, num_sms, 8).total, layout(B, H, H_kv, N_q, d, num_sms, 16).total);
 }
 
 std::once_flag g_once[64];
@@ -260,7 +269,7 @@ int fa_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, 
 size_t fa_fwd_kv4_workspace_size(int B, int H, int H_kv, int N_q, int d) {
     if (B <= 0 || H <= 0 || H_kv <= 0 || N_q <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
     if (B > 65535 || H > 65535) return 0;
-    return layout(B, H, H_kv, N_q, d, fa_internal::current_num_sms()).total;
+    return workspace_size(B, H, H_kv, N_q, d, fa_internal::current_num_sms());
 }
 
 int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
@@ -285,8 +294,7 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     int dev = -1, sms = 0;
     st = ready_device(&dev, &sms);
     if (st != FA_OK) sms = fa_internal::current_num_sms();
-    const Layout L = layout(B, H, H_kv, N_q, d, sms);
-    if (workspace_bytes < L.total) return FA_ERR_INVALID_ARG;
+    if (workspace_bytes < workspace_size(B, H, H_kv, N_q, d, sms)) return FA_ERR_INVALID_ARG;
     if (st == FA_OK) st = prepare_attend(dev);
     if (st != FA_OK) return st;
     kv4::Rows rows{};
@@ -300,6 +308,8 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     long long keys = (long long)max_pages * page_size;
     if (window_left >= 0) keys = std::min(keys, (long long)rows.window + N_q);
+    const int rb = row_block(R, (long long)B * H_kv, keys, sms);
+    const Layout L = layout(B, H, H_kv, N_q, d, sms, rb);
     const int splits = key_splits(R, (long long)B * H_kv, sms, keys);
     if (many_rows(R, (long long)B * H_kv, splits, sms, keys)) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -319,7 +329,6 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
         p.part_ml = reinterpret_cast<float*>(ws + L.rows_ml);
         return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
     }
-    const int rb = row_block(R, (long long)B * H_kv);
     kv4::AttendParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k_codes = static_cast<const uint8_t*>(k_codes);

@@ -351,6 +351,11 @@ ATTEND = [
     (3, 4, 2, 24, 128, 48, 70, [3300, 0, 50], None, False, -1),       # ranges without a key
     (1, 10, 5, 140, 64, 64, 40, [2222], [131], True, 700),            # ranges that windows leave out
     (1, 1, 1, 300, 128, 16, 160, [2500], None, True, -1),
+    # room for much longer sequences and many heads: sixteen rows a block
+    (8, 24, 8, 4, 128, 64, 128, [300, 0, 17, 2000, 129, 1, 777, 64], [4, 4, 0, 1, 3, 4, 4, 2], True, -1),
+    (16, 16, 4, 4, 64, 16, 512, [(211 * b) % 1500 for b in range(16)], None, False, 100),
+    (8, 64, 8, 2, 64, 48, 180, [5, 900, 48, 47, 2, 333, 1000, 96], None, True, -1),
+    (8, 9, 9, 10, 128, 32, 256, [40, 1, 9, 10, 500, 128, 129, 127], None, True, 20),
 ]
 
 
@@ -412,6 +417,30 @@ def test_what_a_query_does_not_see_has_no_influence(H_kv, N, rows, page):
     c = filled(1, H_kv, page, 128, 13, key_lens, 34, edit=edit2)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), key_lens, None, 0.09, True, 8)
     check(c, bits, key_lens, None, 0.09, True, 8, o, lse, heads=heads)
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32)])
+def test_poisoned_keys_and_missing_pages_with_sixteen_rows_a_block(d, page):
+    import torch
+    B, H_kv, N, n, pages = 8, 8, 12, 230, 8192 // page
+    def edit(k, v):
+        k[:, :, n - 2, 5] = 0x7FC0
+        v[:, :, n - 1, 40] = 0x7F80
+        v[:, :, 100, 9] = 0xFF80
+    table = np.random.default_rng(45).permutation(B * pages).reshape(B, pages)
+    lens = [n, n, n - 1, n - 2, 101, 100, 0, n]
+    c = filled(B, H_kv, page, d, pages, [n] * B, 45, table=table, edit=edit)
+    bits = normal_bf16((B, H_kv, N, d), 46, 0)
+    q = to_device_bf16(bits)
+    for window in (-1, 40):
+        o, lse, _ = run_kv4(c, q, lens, None, 0.09, True, window)
+        check(c, bits, lens, None, 0.09, True, window, o, lse, heads=[0, H_kv - 1], what=str(window))
+    assert torch.isfinite(o[5].float()).all() and torch.isnan(o[0, :, -1].float()).all()
+    table[:, 2] = -1
+    c.table[...] = table
+    c.d_table.copy_(ints(table))
+    o, lse, _ = run_kv4(c, q, lens, [12, 5, 0, 12, 12, 12, 1, 1], 0.09, True, -1)
+    check(c, bits, lens, [12, 5, 0, 12, 12, 12, 1, 1], 0.09, True, -1, o, lse, heads=[0, H_kv - 1])
 
 
 @pytest.mark.parametrize("H,N", [(2, 1), (2, 3), (8, 30)])       # merged parts; ranges of keys
@@ -516,7 +545,7 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(lse.cpu().numpy()[0, h] - rl) <= el)
 
 
-@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 5), (2, 40), (16, 70)])
+@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 5), (2, 40), (16, 70), (64, 4)])
 def test_results_are_the_same_bits_each_time_and_on_another_stream(H_kv, N):
     import torch
     key_lens = [1900, 5, 777]
