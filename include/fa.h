@@ -400,7 +400,9 @@ FA_API int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, v
  * which is exactly a bf16 number, |s|/2 from x at most, or 1.25 |s| next to -m, for which
  * there is no code (0.56 bytes an element instead of 2).  A group that holds a value that
  * is not finite, or above 2^120 in magnitude, stands for NaN; one whose values are all
- * below 2^-107 stands for zeros.
+ * below 2^-107 stands for zeros.  Scales come from fa_kv4_append; one of 2^118 or more
+ * in magnitude, which it never writes, stands for NaN (memory that was never written may
+ * hold any; see what fa_fwd_kv4 says of keys that a query does not see).
  *
  * Sequences and pages:
  *   block_table  device int32 [B, max_pages]: the pages of each sequence in order; NULL:

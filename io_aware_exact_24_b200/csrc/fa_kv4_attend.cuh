@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (pos + 16 * j + t + 4 * i >= x.kl || !half_there(j)) sv[i] = 0;
-                    bad |= (sv[i] & 0x7fffu) > 0x7f80u;
+                    bad |= no_scale(sv[i]);
                 }
                 poisoned = __any_sync(0xffffffffu, bad);
             }

@@ -11,6 +11,8 @@
 // the 8 bits of a bf16: the value is exact in bf16, reading back rounds nothing, and the
 // tensor cores get the operand that the definition names.  The sign of s puts the group's
 // extreme value on the code -8, which has no positive partner; 4 + 16/32 bits an element.
+// s is at most 2^117; a scale of 2^118 or more in magnitude (memory that was never written may
+// hold any) stands for NaN, as an infinite one does.
 #pragma once
 
 #include <cstdint>
@@ -25,6 +27,7 @@ constexpr int kGroup = 32;                       // channels per scale
 constexpr uint32_t kMagLargest = 0x7b80;         // bf16 bits of 2^120: a group above it (or not finite) reads back as NaN
 constexpr uint32_t kMagSmallest = 0x0a00;        // bf16 bits of 2^-107: a group below it reads back as zeros
 constexpr uint32_t kScaleNaN = 0x7fc0;
+constexpr uint32_t kScaleNone = 0x7a80;          // bf16 bits of 2^118: the magnitude from which on a scale stands for NaN
 
 // Every kernel here begins with this: the next kernel of the stream may be set up from now on
 // (where it allows that), and the memory of the kernels before is complete.  For calls one after
@@ -164,11 +167,23 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(int i, uint32_t w, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(t), "r"(s2), "r"(m24s2));
     return r;
 }
+// -24 s, exact for 5 significant bits, as 1024 s - 131/128 * 1024 s: from |s| = 2^118 on 1024 s is
+// infinite and this, and so every code, NaN.  (With a plain -24 s a hidden scale of 2^123.4 or more
+// would give codes of -inf, and 0 * inf NaN in the rows that do not see it.)
 __device__ __forceinline__ uint32_t minus_24(uint32_t s2) {
+    uint32_t t, r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t) : "r"(s2), "r"(0x44804480u));                  // 1024
+    asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(r) : "r"(t), "r"(0xBF83BF83u));               // -131/128
+    return r;
+}
+// The same in one instruction, of scales below 2^118.
+__device__ __forceinline__ uint32_t minus_24_of_a_number(uint32_t s2) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(s2), "r"(0xC1C0C1C0u));
     return r;
 }
+// Whether a scale stands for NaN.
+__device__ __forceinline__ bool no_scale(uint32_t s) { return (s & 0x7fffu) >= kScaleNone; }
 
 // ---------------------------------------------------------------- writing the cache
 // Both kernels below give a thread 8 channels of a token.  With many tokens a head, block

@@ -30,6 +30,8 @@
 // epilogue and join: 8 x 128 rows on 700 keys, 12.5 us.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_kernel.cuh"
 #include "fa_kv4_kernel.cuh"
 
@@ -262,8 +264,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             return (uint32_t)v;
         };
         const uint32_t at_s = stage + (uint32_t)(C::kStageS + key_l * kSRow + grp * 2);
-        auto store = [&](uint32_t slot, int o, const uint4& c, uint32_t s) {
-            const uint32_t s2 = __byte_perm(s, s, 0x1010), z2 = minus_24(s2);
+        auto store = [&](auto is_k, uint32_t slot, int o, const uint4& c, uint32_t s) {
+            // (V's scales that stand for NaN have been made zeros)
+            const uint32_t s2 = __byte_perm(s, s, 0x1010), z2 = decltype(is_k)::value ? minus_24(s2) : minus_24_of_a_number(s2);
             const int key = w * 32 + o * kKeys + key_l;
             const uint32_t at = slot + (uint32_t)((grp >> 1) * F::kBoxBytes + key * 128);
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 sc[o] = lds2(at_s + o * kKeys * kSRow);
                 v_sc[o] = lds2(at_s + 32 * kSRow + o * kKeys * kSRow);
                 if (o * kKeys >= left || row[o / kRunPass] == 0xffffffffu) v_sc[o] = 0;
-                bad |= (v_sc[o] & 0x7f80u) == 0x7f80u;
+                bad |= no_scale(v_sc[o]);
             }
             __syncwarp();
             if (j + 1 < n_kv) rows_of(j + 1);
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 uint32_t word = 0;           // lane g's: the 32 keys' bits of group g
 #pragma unroll
                 for (int o = 0; o < kPass; ++o) {
-                    const bool is = (v_sc[o] & 0x7f80u) == 0x7f80u;
+                    const bool is = no_scale(v_sc[o]);
                     const uint32_t bal = __ballot_sync(0xffffffffu, is);
                     if (lane < kG) word |= ((bal >> (lane * kKeys)) & ((1u << kKeys) - 1u)) << (o * kKeys);
                     if (is) v_sc[o] = 0;
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             }
             if (lane == 0) note(j)[w] = gone | (any_bad ? 4u : 0u);
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(0, sl), o, cw[o], sc[o]);
+            for (int o = 0; o < kPass; ++o) store(std::true_type{}, ring_slot(0, sl), o, cw[o], sc[o]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_full(0, sl));
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             ok = __all_sync(0xffffffffu, wait_bounded(bar_empty(1, sl), ((uint32_t)(j / F::kStagesV) & 1u) ^ 1u, abort_flag, p.wait_limit));
             if (!ok) break;
 #pragma unroll
-            for (int o = 0; o < kPass; ++o) store(ring_slot(1, sl), o, cw[o], sc[o]);
+            for (int o = 0; o < kPass; ++o) store(std::false_type{}, ring_slot(1, sl), o, cw[o], sc[o]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_full(1, sl));

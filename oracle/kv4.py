@@ -8,7 +8,8 @@ one row at a time where that is the plainest way to say it:
     code = clamp(rint(x / s), -8, 7) + 8, ties to even; it stands for (code - 8) * s
 
 A group that holds a value that is not finite or above 2^120 stands for NaN, one whose values
-are all below 2^-107 for zeros.
+are all below 2^-107 for zeros.  A scale of 2^118 or more in magnitude, which no group has, stands
+for NaN too.
 """
 from __future__ import annotations
 
@@ -43,7 +44,9 @@ def quantise(x: np.ndarray):
 
 def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     """What codes [..., d] with scales [..., d/32] stand for (float64)."""
-    return (codes.astype(np.float64) - 8.0) * np.repeat(np.asarray(scales, np.float64), GROUP, axis=-1)
+    s = np.asarray(scales, np.float64)
+    s = np.where(np.abs(s) < 2.0 ** 118, s, np.nan)
+    return (codes.astype(np.float64) - 8.0) * np.repeat(s, GROUP, axis=-1)
 
 
 def pack(codes: np.ndarray) -> np.ndarray:

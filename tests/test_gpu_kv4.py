@@ -720,3 +720,77 @@ def test_lengths_below_zero_are_empty():
     bits = normal_bf16((2, 2, 3, 64), 98, 0)
     o, lse, _ = run_kv4(c, to_device_bf16(bits), [-1, 0], [-5, 3], 0.1, True, -1)
     assert (kb == 0).all() and (vb == 0).all() and (o == 0).all() and torch.isneginf(lse).all()
+
+
+# ---------------------------------------------------------------- scales that the format has not
+
+# bf16 bits: finite ones from 2^118 on, the first that overflows times 24, infinities, NaN
+NO_SCALES = [0x7A80, 0xFB00, 0x7D2B, 0x7D80, 0x7F00, 0xFF00, 0x7F7F, 0x7F80, 0xFF80, 0x7FC0]
+
+
+def bf16_of(bits):
+    import torch
+    return torch.tensor(np.array(bits, np.uint16).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,H_kv,N", [(1, 1, 1), (2, 2, 3), (4, 2, 12), (8, 4, 20), (32, 32, 150), (4, 1, 150)])
+def test_rows_that_were_never_written_have_no_influence(H, H_kv, N, d, page):
+    """A layer with a window appends the last tokens of a prompt alone: the rows before them, in the
+    same page and the same tile, are whatever the memory held, and so are those behind the last token."""
+    import torch
+    n, window, B, maxp = 30 * page + 13, 7, 2, 32            # no query sees a position before n - N - window
+    rand = torch.Generator(device="cuda")
+    rand.manual_seed(107)
+    bits = normal_bf16((B, H, N, d), 102, 0)
+    q = to_device_bf16(bits)
+    (k, v), _ = tokens(B, H_kv, N + window, d, 103)
+    table = np.random.default_rng(104).permutation(B * maxp).reshape(B, maxp)
+    for i, scale in enumerate(NO_SCALES):
+        c = Cache(B * maxp, H_kv, page, d, maxp, table)
+        for codes, scales in ((c.k_codes, c.k_scales), (c.v_codes, c.v_scales)):
+            codes.random_(generator=rand)
+            scales[...] = bf16_of([scale])[0]
+        c.append(k, v, [n, n], [N + window] * B)
+        for causal, w in ((True, window), (False, window)):
+            o, lse, guards = run_kv4(c, q, [n, n], None, 0.11, causal, w)
+            assert guards
+            assert not np.isnan(to_host_f64(o)).any() and np.isfinite(lse.cpu().numpy()).all(), hex(scale)
+            if i < 2:
+                check(c, bits, [n, n], None, 0.11, causal, w, o, lse, heads=sorted({0, H - 1}), what=hex(scale))
+
+
+@pytest.mark.parametrize("H_kv,N", [(2, 1), (2, 12), (2, 20), (32, 150)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32)])
+def test_a_scale_that_append_cannot_write_stands_for_nan(H_kv, N, d, page):
+    """The queries that see such a group get NaN, in its channels where it is V's; the others do not."""
+    import torch
+    n = 9 * page + 5
+    bits = normal_bf16((1, H_kv, N, d), 105, 0)
+    q = to_device_bf16(bits)
+    clean = filled(1, H_kv, page, d, 10, [n], 106)
+    for what in ("k", "v"):
+        # the largest below 2^118, and the largest of five bits.  The products of a scale of more bits
+        # are not exact: 24 s is rounded by at most 2^-8 of it, and that is all that is left of a code 8
+        for scale in NO_SCALES + [0x7A7F, 0x7A78]:
+            number = scale not in NO_SCALES
+            c = Cache(11, H_kv, page, d, 10, clean.table)
+            for a, b in zip(c.buffers, clean.buffers):
+                a.copy_(b)
+            at, off = kv4.place(n - 1, 0, c.table, page, 10, 11)
+            codes, scales = (c.k_codes, c.k_scales) if what == "k" else (c.v_codes, c.v_scales)
+            codes[at, :, off] = 0x88                                  # every code stands for 0 * s
+            scales[at, :, off, 1] = bf16_of([scale])[0]
+            kb, vb = c.read([n], n)
+            got = to_host_f64(kb if what == "k" else vb)[0, :, n - 1]
+            assert np.isnan(got[:, 32:64]).all() != number and not np.isnan(got[:, :32]).any()
+            if number:
+                assert (np.abs(got[:, 32:64]) <= (24 * 2.0 ** 110 * 255 if scale == 0x7A7F else 0) * 2.0 ** -8).all()
+            o, lse, _ = run_kv4(c, q, [n], None, 0.11, True, -1)
+            if scale != 0x7A7F:
+                check(c, bits, [n], None, 0.11, True, -1, o, lse, heads=[0, H_kv - 1], what=what + hex(scale))
+            o = to_host_f64(o)
+            assert not np.isnan(o[:, :, :-1]).any()
+            assert np.isnan(o[:, :, -1, 32:64]).all() != number
+    torch.cuda.synchronize()

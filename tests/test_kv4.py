@@ -93,6 +93,43 @@ def test_ends_of_the_range(bad, want):
         assert y[0, 7] == bad
 
 
+@pytest.mark.parametrize("s,nan", [(2.0 ** 117, False), (2.0 ** 118 - 2.0 ** 110, False), (2.0 ** 118, True), (-2.0 ** 124, True),
+                                   (np.inf, True), (-np.inf, True), (np.nan, True)])
+def test_scales_that_the_format_has_not(s, nan):
+    # the largest that a group can have is 2^117 (of 2^120); of foreign ones, 2^118 is the first to stand for NaN
+    y = kv4.values(np.arange(16, dtype=np.uint8).repeat(2)[None], np.array([[s]]))
+    assert np.all(np.isnan(y)) if nan else np.array_equal(y[0], (np.arange(16).repeat(2) - 8.0) * s)
+
+
+def bf16_round(x):
+    """float64 to the bf16 numbers, ties to even, past 2^128 - 2^119 to infinity."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(all="ignore"):
+        m, e = np.frexp(x)
+        e = np.maximum(e, -125)                  # subnormal numbers are multiples of 2^-133
+        y = np.ldexp(np.rint(np.ldexp(x, 8 - e)), e - 8)
+    y = np.where(np.isfinite(x), y, x)
+    return np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, x), y)
+
+
+def test_the_arithmetic_of_the_codes_gives_the_format():
+    # what the kernels compute, each step rounded to bf16: t = 1024 s, z = t - 131/128 t (-24 s, or
+    # NaN from |s| = 2^118 on, where t is infinite), and (16 + c) s + z
+    bits = np.arange(1 << 16, dtype=np.uint16)
+    s = bf16_bits_to_f32(bits).astype(np.float64)
+    with np.errstate(all="ignore"):
+        t = bf16_round(s * 1024.0)
+        z = bf16_round(t * (-131.0 / 128.0) + t)
+        got = [bf16_round((16.0 + c) * s + z) for c in range(16)]
+    five = np.isfinite(s) & (bits & 7 == 0) & (np.abs(s) >= 2.0 ** -110) & (np.abs(s) <= 2.0 ** 117)   # what append writes
+    assert five.sum() == 2 * (227 * 16 + 1)
+    for c in range(16):
+        nan = ~(np.abs(s) < 2.0 ** 118)
+        assert np.array_equal(np.isnan(got[c]), nan)
+        assert np.array_equal(got[c][five], (c - 8) * s[five])
+        assert np.all(np.isfinite(got[c][~nan]))
+
+
 def test_attend_ignores_what_a_query_does_not_see():
     rng = np.random.default_rng(0)
     q, k, v = rng.normal(size=(3, 64)), rng.normal(size=(9, 64)), rng.normal(size=(9, 64))
