@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
             const __nv_bfloat16* q = p.q + (((long long)x.b * p.H_kv + seg_h) * p.rows.R + x.r0) * D;
             for (int i = warp; i < NB * kKW; i += kWarps) {
                 const int r = i / kKW * 8 + g, w = i % kKW;
-                const uint4 y = r < x.nr ? __ldg(reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4)) + w)
+                const uint4 y = r < x.nr ? __ldcg(reinterpret_cast<const uint4*>(q + (long long)r * D + t * (D / 4)) + w)
                                          : make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4*>(qs + i * 512) =
                     make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410),

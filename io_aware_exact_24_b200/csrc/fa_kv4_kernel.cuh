@@ -32,6 +32,9 @@ constexpr uint32_t kScaleNone = 0x7a80;          // bf16 bits of 2^118: the magn
 // Every kernel here begins with this: the next kernel of the stream may be set up from now on
 // (where it allows that), and the memory of the kernels before is complete.  For calls one after
 // another on a stream it hides the setup: 8 heads on 700 keys 10.3 -> 8.1 us a call.
+// A block may thus be on its SM while the kernels before it still write what it will read, so
+// memory is not read-only for its lifetime: no load here may take the non-coherent path (no
+// __ldg, no __restrict__).  What those kernels write (codes, scales, q, k, v, parts) is loaded past L1.
 __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -66,13 +69,13 @@ __device__ __forceinline__ int page_div(const Paging& pg, int n, int& rem) {
 __device__ __forceinline__ int page_of(const Paging& pg, int b, int p) {
     const long long at = (long long)b * pg.max_pages + p;
     if (pg.table == nullptr) return at < pg.num_pages ? (int)at : -1;
-    const int page = __ldg(pg.table + at);
+    const int page = pg.table[at];
     return page >= 0 && page < pg.num_pages ? page : -1;
 }
 
 __device__ __forceinline__ int clamped(const int32_t* p, int b, int top) {
     if (p == nullptr) return top;
-    const int v = __ldg(p + b);
+    const int v = p[b];
     return v < 0 ? 0 : (v > top ? top : v);
 }
 
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
     }
     const int b = bh / p.H_kv, h = bh - b * p.H_kv;
     const int nl = clamped(p.new_lens, b, p.N);
-    const int first = max(0, __ldg(p.key_lens + b)) - nl;    // of the new tokens' positions
+    const int first = max(0, p.key_lens[b]) - nl;    // of the new tokens' positions
     const uint32_t top = (uint32_t)(p.pg.max_pages * p.pg.page_size);
     const uint4* const k = p.k + (long long)bh * p.N * kLanes + sub;
     const uint4* const v = p.v + (long long)bh * p.N * kLanes + sub;
@@ -291,8 +294,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
             row[i] = 0xffffffffu;
             kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
             if (valid && n < nl && (uint32_t)pos < top) {
-                kx[i] = __ldg(k + (size_t)n * kLanes);
-                vx[i] = __ldg(v + (size_t)n * kLanes);
+                kx[i] = __ldcg(k + (size_t)n * kLanes);
+                vx[i] = __ldcg(v + (size_t)n * kLanes);
                 int off;
                 const int page = page_of(p.pg, b, page_div(p.pg, pos, off));
                 if (page >= 0) row[i] = ((uint32_t)page * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size + (uint32_t)off;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
     }
     const int b = bh / p.H_kv, h = bh - b * p.H_kv;
     const int kl = clamped(p.key_lens, b, p.pg.max_pages * p.pg.page_size);
-    const long long first = p.first != nullptr ? (long long)__ldg(p.first + b) : 0;
+    const long long first = p.first != nullptr ? (long long)p.first[b] : 0;
     uint4* const k = p.k + (long long)bh * p.N * kLanes + sub;
     uint4* const v = p.v + (long long)bh * p.N * kLanes + sub;
     for (int n0 = blockIdx.y * (kRows * kEach); n0 < p.N && valid; n0 += kFlat ? p.N : (int)gridDim.y * (kRows * kEach)) {
@@ -372,10 +375,10 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
                 const int page = page_of(p.pg, b, page_div(p.pg, (int)pos, off));
                 if (page >= 0) {
                     const uint32_t row = ((uint32_t)page * (uint32_t)p.H_kv + (uint32_t)h) * (uint32_t)p.pg.page_size + (uint32_t)off;
-                    kw[i] = __ldg(p.k_codes + (size_t)row * kLanes + sub);
-                    vw[i] = __ldg(p.v_codes + (size_t)row * kLanes + sub);
-                    ks[i] = __ldg(p.k_scales + (size_t)row * (D / kGroup) + (sub >> 2));
-                    vs[i] = __ldg(p.v_scales + (size_t)row * (D / kGroup) + (sub >> 2));
+                    kw[i] = __ldcg(p.k_codes + (size_t)row * kLanes + sub);
+                    vw[i] = __ldcg(p.v_codes + (size_t)row * kLanes + sub);
+                    ks[i] = __ldcg(p.k_scales + (size_t)row * (D / kGroup) + (sub >> 2));
+                    vs[i] = __ldcg(p.v_scales + (size_t)row * (D / kGroup) + (sub >> 2));
                 }
             }
         }

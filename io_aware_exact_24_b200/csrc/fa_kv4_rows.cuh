@@ -724,10 +724,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams 
         for (int i = 0; i < kEach; ++i) {
             const size_t a = at + min(s0 + i * kJoinWarps, p.splits - 1);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) ml[i][k] = p.part_ml[(a * 3 + k) * kBlockM + r];
+            for (int k = 0; k < 3; ++k) ml[i][k] = __ldcg(p.part_ml + (a * 3 + k) * kBlockM + r);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float4 f = p.part[(a * (D / 4) + 2 * c8 + k) * kBlockM + r];
+                const float4 f = __ldcg(p.part + (a * (D / 4) + 2 * c8 + k) * kBlockM + r);
                 v[i][4 * k] = f.x, v[i][4 * k + 1] = f.y, v[i][4 * k + 2] = f.z, v[i][4 * k + 3] = f.w;
             }
         }

@@ -794,3 +794,55 @@ def test_a_scale_that_append_cannot_write_stands_for_nan(H_kv, N, d, page):
             assert not np.isnan(o[:, :, :-1]).any()
             assert np.isnan(o[:, :, -1, 32:64]).all() != number
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- calls that overlap
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,n", [(1, 4, 4, 1, 128, 16, 70), (2, 8, 4, 40, 64, 32, 300), (24, 8, 8, 1, 128, 64, 200),
+                                                 (4, 16, 16, 150, 128, 16, 1500)])
+def test_queued_calls_see_what_the_one_before_wrote(B, H, H_kv, N, d, page, n):
+    """read, append of other values at the same positions, read, attend, many times without waiting
+    on the host, and attention on what a read gave back: each call has the answers that it has alone."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
+    maxp, turns, sets = -(-n // page), 30, 3
+    table = ints(np.random.default_rng(111).permutation(B * maxp).reshape(B, maxp))
+    lens, first = ints([n] * B), ints([n - N] * B)
+    base, _ = tokens(B, H_kv, n, d, 112)
+    new = [tokens(B, H_kv, N, d, 113 + i)[0] for i in range(sets)]
+    q = [to_device_bf16(normal_bf16((B, H, N, d), 120 + i, 0)) for i in range(sets)]
+    size = fa_fwd_kv4_workspace_size(B, H, H_kv, N, d)
+    ws = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+    empty = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="cuda")
+
+    def run(wait):
+        c = Cache(B * maxp, H_kv, page, d, maxp, None)
+        again = Cache(B * maxp, H_kv, page, d, maxp, None)
+        out = [[empty(B, H_kv, N, d) for _ in range(4)] + [empty(B, H, N, d), empty(B, H, N, t=torch.float32)] for _ in range(turns)]
+        torch.cuda.synchronize()
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        fa_kv4_append(*base, *c.buffers, table, lens, None, B, H_kv, n, *c.sizes)
+        for i, (k0, v0, k1, v1, o, lse) in enumerate(out):
+            done()
+            fa_kv4_read(*c.buffers, table, lens, first, k0, v0, B, H_kv, N, *c.sizes)
+            done()
+            fa_kv4_append(*new[i % sets], *c.buffers, table, lens, None, B, H_kv, N, *c.sizes)
+            done()
+            fa_kv4_read(*c.buffers, table, lens, first, k1, v1, B, H_kv, N, *c.sizes)
+            done()
+            # what was just read is written to another cache
+            fa_kv4_append(k1, v1, *again.buffers, table, lens, None, B, H_kv, N, *again.sizes)
+            done()
+            fa_fwd_kv4(q[i % sets], *c.buffers, table, lens, None, o, lse, B, H, H_kv, N, *c.sizes, 0.1, True, -1, ws, size)
+        torch.cuda.synchronize()
+        return out + [list(c.buffers), list(again.buffers)]
+
+    want = run(True)
+    for got in (run(False), run(False)):
+        for i, (g, w) in enumerate(zip(got, want)):
+            for j, (a, b) in enumerate(zip(g, w)):
+                a, b = (x.view(torch.int16) if x.dtype == torch.bfloat16 else x for x in (a, b))
+                assert torch.equal(a, b), (i, j)
+    for k0, k1, turn in ((want[i + 1][0], want[i][2], i) for i in range(turns - 1)):
+        assert torch.equal(k0, k1), turn
+        assert turn % sets == 0 or not torch.equal(k0, want[turn - 1][2])

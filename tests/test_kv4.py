@@ -1,5 +1,8 @@
 """CPU tests of the 4-bit key/value cache: the format's oracle against hand-worked groups and
 its own properties, and the refusals of the entry points (no GPU touched)."""
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -153,6 +156,22 @@ def test_places():
     assert kv4.place(17, 3, None, 16, 2, 9) == (7, 1) and kv4.place(17, 4, None, 16, 2, 9) is None
     assert kv4.place(17, 0, [[4, 9]], 16, 2, 9) is None and kv4.place(15, 0, [[4, 9]], 16, 2, 9) == (4, 15)
     assert kv4.place(15, 0, [[-1, 9]], 16, 2, 9) is None
+
+
+# ---------------------------------------------------------------- launches that overlap
+
+def test_kernels_that_overlap_the_one_before_load_nothing_as_read_only():
+    # their blocks may be resident while the kernel before still writes what they will read: the
+    # non-coherent path is for memory that nobody writes during a kernel's lifetime
+    csrc = os.path.join(os.path.dirname(binding.__file__), "csrc")
+    for name in sorted(f for f in os.listdir(csrc) if f.startswith("fa_kv4") and f.endswith(".cuh")):
+        code = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        assert not re.search(r"__ldg\s*\(|\.nc\b|__restrict__", code), name
+        # and each begins by waiting for it: nothing of its parameters' memory is touched before
+        for kernel in re.findall(r"__global__[^{]*?(\w+_kernel)\(", code):
+            body = code[code.index(kernel + "("):]
+            before = body[:body.index("after_previous();")]
+            assert not re.search(r"p\.(q|k|v|o|lse|part|part_ml|words|key_lens|\w+_codes|\w+_scales)\b|tma_load|cp_async16", before), kernel
 
 
 # ---------------------------------------------------------------- refusals
