@@ -846,3 +846,25 @@ def test_queued_calls_see_what_the_one_before_wrote(B, H, H_kv, N, d, page, n):
     for k0, k1, turn in ((want[i + 1][0], want[i][2], i) for i in range(turns - 1)):
         assert torch.equal(k0, k1), turn
         assert turn % sets == 0 or not torch.equal(k0, want[turn - 1][2])
+
+
+def test_bad_pages_touch_no_other_page():
+    """A page that two bad entries could be mistaken for, and every row behind the named ones, keep their bits."""
+    import torch
+    c = Cache(5, 2, 16, 64, 3, [[2, -1, 0], [5, 1, (1 << 31) - 1]])
+    (k, v), _ = tokens(2, 2, 48, 64, 12)
+    before = [b.clone() for b in c.buffers]
+    c.append(k, v, [48, 48])
+    torch.cuda.synchronize()
+    named = {0: (0, 32), 2: (0, 0), 1: (1, 16)}              # page: sequence, its first token
+    for got, was, x in zip(c.buffers, before, (k, k, v, v)):
+        for page in range(5):
+            same = torch.equal(got[page].view(torch.uint8), was[page].view(torch.uint8))
+            assert same == (page not in named), page
+    kb, vb = c.read([48, 48], 48)
+    for got, x in ((kb, k), (vb, v)):
+        back = kv4.values(*kv4.quantise(to_host_f64(x)))
+        want = np.zeros_like(back)
+        for b, at in named.values():
+            want[b, :, at:at + 16] = back[b, :, at:at + 16]
+        assert np.array_equal(to_host_f64(got), want)
