@@ -474,6 +474,7 @@ FA_API int fa_kv4_read(const void *k_codes, const void *k_scales, const void *v_
  *              may be replayed, and graphs that are ordered may share one.
  * K and V of a key that a query does not see have no influence on it, whatever they hold.
  * For a given device the result depends on the arguments alone, bit for bit.
+ * A wait inside a kernel that runs out (see fa_get_device_status) makes the rows concerned NaN.
  * Returns as fa_fwd; FA_ERR_INVALID_ARG also for H not a multiple of H_kv, a NULL or short
  * workspace.  B, H or N_q equal to 0 is a no-op.
  */
@@ -542,6 +543,24 @@ FA_API int fa_selftest_bwd_timeout(const void *q, const void *k, const void *v, 
                                    const float *lse, const void *dout, void *dq, void *dk,
                                    void *dv, int B, int H, int N_q, int N_k, int d, float scale,
                                    int causal, void *workspace, size_t workspace_bytes,
+                                   unsigned long long limit_cycles, fa_stream_t stream);
+
+/*
+ * fa_selftest_kv4_timeout -- failure-detection self test of fa_fwd_kv4's kernel for many
+ * query rows (the others wait for nothing but their own copies).  Runs fa_fwd_kv4
+ * (arguments as there) with every wait bounded by `limit_cycles` SM clock cycles (1 ..
+ * 2^32), synchronises `stream` and returns what fa_get_device_status reports, as
+ * fa_selftest_fwd_timeout does.  Every row of o and lse then holds the answer, or NaN where
+ * a wait of its block, or of one of the ranges of keys that are joined for it, ran out.
+ * FA_ERR_INVALID_ARG for a call that the kernel for few rows would take.
+ */
+FA_API int fa_selftest_kv4_timeout(const void *q, const void *k_codes, const void *k_scales,
+                                   const void *v_codes, const void *v_scales,
+                                   const int32_t *block_table, const int32_t *key_lens,
+                                   const int32_t *q_lens, void *o, float *lse, int B, int H,
+                                   int H_kv, int N_q, int d, int num_pages, int page_size,
+                                   int max_pages, float scale, int causal, int window_left,
+                                   void *workspace, size_t workspace_bytes,
                                    unsigned long long limit_cycles, fa_stream_t stream);
 
 /*

@@ -113,6 +113,8 @@ def load_library() -> ctypes.CDLL:
             lib.fa_selftest_bwd_timeout.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32,
                                                     i32, i32, f32, i32, vp, sz, ctypes.c_ulonglong, vp]
             lib.fa_selftest_bwd_timeout.restype = i32
+            lib.fa_selftest_kv4_timeout.argtypes = [vp] * 10 + [i32] * 8 + [f32, i32, i32, vp, sz, ctypes.c_ulonglong, vp]
+            lib.fa_selftest_kv4_timeout.restype = i32
             lib.fa_last_error.argtypes = []
             lib.fa_last_error.restype = ctypes.c_char_p
             lib.fa_version.argtypes = []
@@ -389,6 +391,16 @@ def fa_selftest_bwd_timeout(q, k, v, o, lse, dout, dq, dk, dv, B, H, N_q, N_k, d
         _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(dout), _addr(dq), _addr(dk),
         _addr(dv), int(B), int(H), int(N_q), int(N_k), int(d), float(scale), int(bool(causal)),
         _addr(workspace), int(workspace_bytes), int(limit_cycles), _stream(stream)))
+
+
+def fa_selftest_kv4_timeout(q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o,
+                            lse, B, H, H_kv, N_q, d, num_pages, page_size, max_pages, scale, causal,
+                            window_left, workspace, workspace_bytes, limit_cycles, stream=None) -> int:
+    """``fa_selftest_kv4_timeout`` of include/fa.h: 4-bit cache attention for many rows, short wait limit."""
+    return int(load_library().fa_selftest_kv4_timeout(
+        *map(_addr, (q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o, lse)),
+        *map(int, (B, H, H_kv, N_q, d, num_pages, page_size, max_pages)), float(scale), int(bool(causal)),
+        int(window_left), _addr(workspace), int(workspace_bytes), int(limit_cycles), _stream(stream)))
 
 
 def attention(q, k, v, causal=False, key_lens=None, scale=None, stream=None):

@@ -631,7 +631,7 @@ int launch_kv4_rows(const void* q, void* o, int B, int d, fa::kv4::RowsParams p,
         snprintf(t_last_error, sizeof t_last_error, "cuTensorMapEncodeTiled failed");
         return FA_ERR_CUDA;
     }
-    p.wait_limit = kWaitLimitCycles;
+    if (p.wait_limit == 0) p.wait_limit = kWaitLimitCycles;
     p.row_blocks = (p.rows.R + fa::kBlockM - 1) / fa::kBlockM;
     p.split_inv = (65535 + p.splits) / p.splits;
     const bool one = p.pg.page_size % 32 == 0;

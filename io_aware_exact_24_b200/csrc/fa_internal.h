@@ -12,7 +12,7 @@ struct RowsParams;
 namespace fa_internal {
 
 // Launches the 4-bit cache attention for many rows (fa_kv4_rows.cuh): q and o are bf16
-// [B, H_kv, rows, d].  p.wait_limit is set here.
+// [B, H_kv, rows, d].  A p.wait_limit of 0 is the default.
 int launch_kv4_rows(const void* q, void* o, int B, int d, fa::kv4::RowsParams p, cudaStream_t stream);
 
 // Records a failed CUDA call for fa_last_error on this thread; returns FA_ERR_CUDA.

@@ -194,6 +194,104 @@ cudaError_t launch_attend(const kv4::AttendParams& p, int rb, bool groups, int n
     return groups ? launch_attend<D, 1, true>(p, num_sms, s) : launch_attend<D, 1, false>(p, num_sms, s);
 }
 
+// fa_fwd_kv4; with wait_limit > 0 only by the kernel for many rows, whose waits it bounds.
+int fwd(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+        const int32_t* block_table, const int32_t* key_lens, const int32_t* q_lens, void* o, float* lse, int B,
+        int H, int H_kv, int N_q, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
+        int window_left, void* workspace, size_t workspace_bytes, fa_stream_t stream,
+        unsigned long long wait_limit) {
+    bool empty = false;
+    int st = validate(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, B, H_kv, N_q, d, num_pages,
+                      page_size, max_pages, &empty);
+    if (st != FA_OK) return st;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(scale) || !(scale > 0.f) || !(scale_log2 > 0.f) || !std::isfinite(scale_log2))
+        return FA_ERR_INVALID_ARG;
+    if (H < 0 || (H_kv > 0 && H % H_kv != 0) || (H_kv == 0 && H != 0)) return FA_ERR_INVALID_ARG;
+    if (empty || H == 0) return wait_limit > 0 ? FA_ERR_INVALID_ARG : FA_OK;
+    if (H > 65535) return FA_ERR_UNSUPPORTED;
+    const long long R = (long long)(H / H_kv) * N_q;
+    const long long units = (long long)max_pages * page_size / kv4::kUnit + 2;   // most of one row block
+    if (R > 0x3fffffffLL || units * H_kv > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
+    if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return FA_ERR_MISALIGNED;
+    int dev = -1, sms = 0;
+    st = ready_device(&dev, &sms);
+    if (st != FA_OK) sms = fa_internal::current_num_sms();
+    if (workspace_bytes < workspace_size(B, H, H_kv, N_q, d, sms)) return FA_ERR_INVALID_ARG;
+    if (st == FA_OK) st = prepare_attend(dev);
+    if (st != FA_OK) return st;
+    kv4::Rows rows{};
+    rows.key_lens = key_lens;
+    rows.q_lens = q_lens;
+    rows.N_q = N_q;
+    rows.R = (int)R;
+    rows.causal = causal ? 1 : 0;
+    rows.window = window_left < 0 ? -1 : std::min(window_left, kMaxPositions);
+    const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    long long keys = (long long)max_pages * page_size;
+    if (window_left >= 0) keys = std::min(keys, (long long)rows.window + N_q);
+    const int rb = row_block(R, (long long)B * H_kv, keys, sms);
+    const Layout L = layout(B, H, H_kv, N_q, d, sms, rb);
+    const int splits = key_splits(R, (long long)B * H_kv, sms, keys);
+    const bool many = many_rows(R, (long long)B * H_kv, splits, sms, keys);
+    if (wait_limit > 0 && !many) return FA_ERR_INVALID_ARG;   // nothing would wait
+    if (many) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        kv4::RowsParams p{};
+        p.k_codes = static_cast<const uint8_t*>(k_codes);
+        p.k_scales = static_cast<const uint16_t*>(k_scales);
+        p.v_codes = static_cast<const uint8_t*>(v_codes);
+        p.v_scales = static_cast<const uint16_t*>(v_scales);
+        p.pg = pg;
+        p.rows = rows;
+        p.H_kv = H_kv;
+        p.o = static_cast<__nv_bfloat16*>(o);
+        p.lse = lse;
+        p.scale_log2 = scale_log2;
+        p.splits = splits;
+        p.wait_limit = wait_limit;
+        p.part = reinterpret_cast<float*>(ws);
+        p.part_ml = reinterpret_cast<float*>(ws + L.rows_ml);
+        return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
+    }
+    kv4::AttendParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_codes = static_cast<const uint8_t*>(k_codes);
+    p.k_scales = static_cast<const uint16_t*>(k_scales);
+    p.v_codes = static_cast<const uint8_t*>(v_codes);
+    p.v_scales = static_cast<const uint16_t*>(v_scales);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.pg = pg;
+    p.H_kv = H_kv;
+    p.rows = rows;
+    p.row_blocks = (int)((R + rb - 1) / rb);
+    p.scale_log2 = scale_log2;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.part_ml = reinterpret_cast<float*>(ws + L.ml);
+    p.words = reinterpret_cast<unsigned long long*>(ws + L.words);
+    p.group_words = reinterpret_cast<unsigned long long*>(ws + L.group_words);
+    const long long entries = (long long)B * p.row_blocks;
+    // the line of units of one launch stays within int
+    const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
+    for (long long e0 = 0; e0 < entries; e0 += chunk) {
+        p.b0 = (int)(e0 / p.row_blocks);
+        p.rb0 = (int)(e0 % p.row_blocks);
+        p.E = (int)std::min(chunk, entries - e0);
+        p.ticket = next_ticket();
+        // parts of an item, if the sequences are alike
+        const long long parts = std::min<long long>((keys + kv4::kUnit - 1) / kv4::kUnit, (long long)sms * ctas_per_sm(rb) / (p.E * H_kv));
+        const int nr = (int)std::min<long long>(R, rb);
+        const bool groups = parts > kv4::kFlat * (d == 64 ? kv4::row_groups<64>(nr) : kv4::row_groups<128>(nr));
+        const cudaError_t e = d == 64 ? launch_attend<64>(p, rb, groups, sms, s) : launch_attend<128>(p, rb, groups, sms, s);
+        if (e != cudaSuccess) return cuda_fail("kernel launch (4-bit cache attention)", e);
+    }
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -276,93 +374,21 @@ int fa_fwd_kv4(const void* q, const void* k_codes, const void* k_scales, const v
                const int32_t* block_table, const int32_t* key_lens, const int32_t* q_lens, void* o, float* lse, int B,
                int H, int H_kv, int N_q, int d, int num_pages, int page_size, int max_pages, float scale, int causal,
                int window_left, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
-    bool empty = false;
-    int st = validate(k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, B, H_kv, N_q, d, num_pages,
-                      page_size, max_pages, &empty);
-    if (st != FA_OK) return st;
-    const float scale_log2 = scale * 1.4426950408889634f;
-    if (!std::isfinite(scale) || !(scale > 0.f) || !(scale_log2 > 0.f) || !std::isfinite(scale_log2))
-        return FA_ERR_INVALID_ARG;
-    if (H < 0 || (H_kv > 0 && H % H_kv != 0) || (H_kv == 0 && H != 0)) return FA_ERR_INVALID_ARG;
-    if (empty || H == 0) return FA_OK;
-    if (H > 65535) return FA_ERR_UNSUPPORTED;
-    const long long R = (long long)(H / H_kv) * N_q;
-    const long long units = (long long)max_pages * page_size / kv4::kUnit + 2;   // most of one row block
-    if (R > 0x3fffffffLL || units * H_kv > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
-    if (q == nullptr || o == nullptr || lse == nullptr || workspace == nullptr) return FA_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return FA_ERR_MISALIGNED;
-    int dev = -1, sms = 0;
-    st = ready_device(&dev, &sms);
-    if (st != FA_OK) sms = fa_internal::current_num_sms();
-    if (workspace_bytes < workspace_size(B, H, H_kv, N_q, d, sms)) return FA_ERR_INVALID_ARG;
-    if (st == FA_OK) st = prepare_attend(dev);
-    if (st != FA_OK) return st;
-    kv4::Rows rows{};
-    rows.key_lens = key_lens;
-    rows.q_lens = q_lens;
-    rows.N_q = N_q;
-    rows.R = (int)R;
-    rows.causal = causal ? 1 : 0;
-    rows.window = window_left < 0 ? -1 : std::min(window_left, kMaxPositions);
-    const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    long long keys = (long long)max_pages * page_size;
-    if (window_left >= 0) keys = std::min(keys, (long long)rows.window + N_q);
-    const int rb = row_block(R, (long long)B * H_kv, keys, sms);
-    const Layout L = layout(B, H, H_kv, N_q, d, sms, rb);
-    const int splits = key_splits(R, (long long)B * H_kv, sms, keys);
-    if (many_rows(R, (long long)B * H_kv, splits, sms, keys)) {
-        uint8_t* ws = static_cast<uint8_t*>(workspace);
-        kv4::RowsParams p{};
-        p.k_codes = static_cast<const uint8_t*>(k_codes);
-        p.k_scales = static_cast<const uint16_t*>(k_scales);
-        p.v_codes = static_cast<const uint8_t*>(v_codes);
-        p.v_scales = static_cast<const uint16_t*>(v_scales);
-        p.pg = pg;
-        p.rows = rows;
-        p.H_kv = H_kv;
-        p.o = static_cast<__nv_bfloat16*>(o);
-        p.lse = lse;
-        p.scale_log2 = scale_log2;
-        p.splits = splits;
-        p.part = reinterpret_cast<float*>(ws);
-        p.part_ml = reinterpret_cast<float*>(ws + L.rows_ml);
-        return fa_internal::launch_kv4_rows(q, o, B, d, p, s);
-    }
-    kv4::AttendParams p{};
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k_codes = static_cast<const uint8_t*>(k_codes);
-    p.k_scales = static_cast<const uint16_t*>(k_scales);
-    p.v_codes = static_cast<const uint8_t*>(v_codes);
-    p.v_scales = static_cast<const uint16_t*>(v_scales);
-    p.o = static_cast<__nv_bfloat16*>(o);
-    p.lse = lse;
-    p.pg = pg;
-    p.H_kv = H_kv;
-    p.rows = rows;
-    p.row_blocks = (int)((R + rb - 1) / rb);
-    p.scale_log2 = scale_log2;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.part = reinterpret_cast<float*>(ws + L.part);
-    p.part_ml = reinterpret_cast<float*>(ws + L.ml);
-    p.words = reinterpret_cast<unsigned long long*>(ws + L.words);
-    p.group_words = reinterpret_cast<unsigned long long*>(ws + L.group_words);
-    const long long entries = (long long)B * p.row_blocks;
-    // the line of units of one launch stays within int
-    const long long chunk = std::min<long long>(kv4::kMaxEntries, std::max<long long>(1, 0x3fffffffLL / (units * H_kv)));
-    for (long long e0 = 0; e0 < entries; e0 += chunk) {
-        p.b0 = (int)(e0 / p.row_blocks);
-        p.rb0 = (int)(e0 % p.row_blocks);
-        p.E = (int)std::min(chunk, entries - e0);
-        p.ticket = next_ticket();
-        // parts of an item, if the sequences are alike
-        const long long parts = std::min<long long>((keys + kv4::kUnit - 1) / kv4::kUnit, (long long)sms * ctas_per_sm(rb) / (p.E * H_kv));
-        const int nr = (int)std::min<long long>(R, rb);
-        const bool groups = parts > kv4::kFlat * (d == 64 ? kv4::row_groups<64>(nr) : kv4::row_groups<128>(nr));
-        const cudaError_t e = d == 64 ? launch_attend<64>(p, rb, groups, sms, s) : launch_attend<128>(p, rb, groups, sms, s);
-        if (e != cudaSuccess) return cuda_fail("kernel launch (4-bit cache attention)", e);
-    }
-    return FA_OK;
+    return fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o, lse, B, H, H_kv, N_q, d, num_pages,
+               page_size, max_pages, scale, causal, window_left, workspace, workspace_bytes, stream, 0);
+}
+
+int fa_selftest_kv4_timeout(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                            const void* v_scales, const int32_t* block_table, const int32_t* key_lens,
+                            const int32_t* q_lens, void* o, float* lse, int B, int H, int H_kv, int N_q, int d,
+                            int num_pages, int page_size, int max_pages, float scale, int causal, int window_left,
+                            void* workspace, size_t workspace_bytes, unsigned long long limit_cycles,
+                            fa_stream_t stream) {
+    if (limit_cycles < 1 || limit_cycles > (1ull << 32)) return FA_ERR_INVALID_ARG;
+    const int st = fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, key_lens, q_lens, o, lse, B, H, H_kv, N_q, d,
+                       num_pages, page_size, max_pages, scale, causal, window_left, workspace, workspace_bytes, stream,
+                       limit_cycles);
+    return st != FA_OK ? st : fa_get_device_status(stream);
 }
 
 }  // extern "C"

@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const bool have_o = n_kv > 0;
         bool good = ok;
         if (good && have_o) {
-            good = __all_sync(0xffffffffu, wait_bounded(bar_drain, 0, abort_flag, p.wait_limit));
+            // (the products' warps end here too when they gave up: then a tile is missing from O)
+            good = __all_sync(0xffffffffu, wait_bounded(bar_drain, 0, abort_flag, p.wait_limit) && *abort_flag == 0);
             if (good) tc_fence_after();
         }
         const int row = (int)part_at[1] + r;
@@ -585,12 +586,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const float f1 = (m1w == m_fin) ? 1.f : ex2_approx(m1w - m_fin);
         const float lu_row = none ? 0.f : epi[2 * kBlockM + r] * f0 + epi[3 * kBlockM + r] * f1;
         if (p.splits > 1) {
-            // (a part that a wait gave up on is an empty one, so that no old contents are joined)
+            // (a part that a wait gave up on has NaN for its sums, and so have the rows that it joins:
+            // an answer that leaves keys out would look like any other)
             const size_t at = part_at[0];
             if (row < p.rows.R && g == 0) {
                 float* const ml = p.part_ml + at * 3 * kBlockM + r;
-                ml[0] = good ? m_fin : -INFINITY;
-                ml[2 * kBlockM] = good ? lu_row : 0.f;
+                ml[0] = good ? m_fin : 0.f;
+                ml[2 * kBlockM] = good ? lu_row : __int_as_float(0x7fc00000);
             }
             if (good && have_o) {
                 uint32_t u[32];
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                         }
                 }
             } else if (row < p.rows.R && g == 0) {
-                p.part_ml[(at * 3 + 1) * kBlockM + r] = 0.f;
+                p.part_ml[(at * 3 + 1) * kBlockM + r] = good ? 0.f : __int_as_float(0x7fc00000);
             }
         } else if (good) {
             float l_row = 0.f;
@@ -666,6 +668,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             for (int bx = 0; bx < F::kOBoxes; ++bx) tma_store_4d(&tm_o, q_tile + bx * kSwizzleBoxBytes, bx * 64, (int)part_at[1], h, b);
             bulk_commit_group();
             bulk_wait_group_read0();
+        }
+        if (any_bad && p.splits == 1 && row < p.rows.R) {   // the whole block's rows, as above
+            const size_t at = ((size_t)b * p.H_kv + h) * (size_t)p.rows.R + row;
+            if (g == 0) p.lse[at] = __int_as_float(0x7fc00000);
+            uint4* const dst = reinterpret_cast<uint4*>(p.o + at * D) + g * (D / 16);
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) dst[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
         }
         tc_fence_before();
     }

@@ -868,3 +868,40 @@ def test_bad_pages_touch_no_other_page():
         for b, at in named.values():
             want[b, :, at:at + 16] = back[b, :, at:at + 16]
         assert np.array_equal(to_host_f64(got), want)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,key_lens", [
+    (1, 8, 1, 5, 128, 32, 200, [6111]),                       # ranges of keys that are joined
+    (2, 4, 2, 33, 64, 16, 300, [4800, 0]),                    # and a sequence without keys
+    (4, 8, 8, 160, 128, 32, 40, [900, 1200, 0, 371]),
+    (64, 2, 2, 130, 64, 16, 40, [(37 * b) % 609 for b in range(64)]),      # one CTA a block of rows
+])
+def test_a_wait_that_runs_out_leaves_nan_and_the_next_call_is_right(B, H, H_kv, N, d, page, maxp, key_lens):
+    """With a wait limit of a few cycles the kernel for many rows winds down; no row has an answer that
+    leaves keys out: it is the right one, bit for bit, or NaN.  The context stays usable."""
+    import torch
+    from io_aware_exact_24_b200 import (FA_ERR_DEVICE_TIMEOUT, FA_ERR_INVALID_ARG, FA_OK, fa_fwd_kv4_workspace_size,
+                                        fa_get_device_status, fa_selftest_kv4_timeout)
+    c = filled(B, H_kv, page, d, maxp, key_lens, 131)
+    bits = normal_bf16((B, H, N, d), 132, 0)
+    q, lens = to_device_bf16(bits), ints(key_lens)
+    n = fa_fwd_kv4_workspace_size(B, H, H_kv, N, d)
+    ws = torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda")      # (numbers, if taken for results)
+    want = run_kv4(c, q, key_lens, None, 0.1, True, -1, workspace=ws)
+    assert fa_get_device_status() == FA_OK
+    for limit in (2, 2, 300, 3000):
+        o, lse = torch.full_like(q, 3.0), torch.full((B, H, N), 3.0, device="cuda")
+        st = fa_selftest_kv4_timeout(q, *c.buffers, c.d_table, lens, None, o, lse, B, H, H_kv, N, *c.sizes, 0.1, True, -1, ws, n, limit)
+        assert st == FA_ERR_DEVICE_TIMEOUT if limit == 2 else st in (FA_ERR_DEVICE_TIMEOUT, FA_OK)
+        assert fa_get_device_status() == FA_OK                # read and cleared by the call
+        same = (o.view(torch.int16) == want[0].view(torch.int16)).all(-1) & (lse == want[1])
+        lost = torch.isnan(o).all(-1) & torch.isnan(lse)
+        assert (same | lost).all(), limit
+        assert lost.any() == (st == FA_ERR_DEVICE_TIMEOUT)
+        o2, lse2, guards = run_kv4(c, q, key_lens, None, 0.1, True, -1, workspace=ws)
+        assert guards and torch.equal(o2.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse2, want[1])
+    assert fa_selftest_kv4_timeout(q, *c.buffers, c.d_table, lens, None, o, lse, B, H, H_kv, 1, *c.sizes, 0.1, True, -1, ws, n,
+                                   2) == FA_ERR_INVALID_ARG
+    check(c, bits, key_lens, None, 0.1, True, -1, *want[:2], heads=[0, H - 1])

@@ -253,6 +253,23 @@ def test_without_a_gpu_valid_calls_report_no_device(lib):
         assert call(num_pages=0, kc=None, ks=None, vc=None, vs=None) == binding.FA_ERR_NO_DEVICE
 
 
+def test_selftest_timeout_argument_errors(lib):
+    def f(limit=2, H=2, N=200, **kw):
+        a = dict(B=1, H_kv=1, num_pages=4, page_size=1024, max_pages=4, key_lens=P, ws=P) | kw
+        return binding.fa_selftest_kv4_timeout(P, P, P, P, P, P, a["key_lens"], P, P, P, a["B"], H, a["H_kv"], N, 64, a["num_pages"],
+                                               a["page_size"], a["max_pages"], 0.125, 1, -1, a["ws"], 1 << 40, limit, stream=0)
+    for kw in (dict(limit=0), dict(limit=(1 << 32) + 1), dict(B=0), dict(N=0), dict(H=0), dict(key_lens=None), dict(ws=None),
+               dict(H_kv=3)):
+        assert f(**kw) == INVALID, kw
+    if not has_gpu():
+        assert f() == binding.FA_ERR_NO_DEVICE
+
+
+def has_gpu():
+    import torch
+    return torch.cuda.is_available()
+
+
 def test_arguments_become_the_same_call(lib):
     """The marshalling module and ctypes hand the library the same values (B = 0: nothing is done)."""
     import ctypes
