@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
     float2 sum[NB];                  // this lane's share of the sums, not rounded
     float ref[NB][2];                // reference max of rows 2t, 2t + 1 (log2 units), equal in all lanes of a t
     float top[NB][2];                // raw score above which the reference moves
-    float2 neg[NB];                  // -ref, or 0 while the row has seen no key
+    float2 neg[NB];                  // -ref - kShift, or 0 while the row has seen no key
     uint8_t* const qs = smem + C::kQOff + lane * 16;
     // MMA row i of a 16-key tile (i < 8) is key i/2 + 4 (i mod 2), row 8 + i that key + 8
     const int key0 = (g >> 1) + 4 * (g & 1);
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     }
         }
         // the reference moves only when some score exceeds it by more than 2^8: until
-        // then probabilities stay below 2^8 and nothing needs to be rescaled
+        // then weights stay below 2^8 times the largest and nothing needs to be rescaled
         bool grow = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -459,9 +459,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     if (m > ref[nb][c]) {
+                        m = reference(m);
                         const float f = ex2_approx(ref[nb][c] - m);   // 0 from a reference of -inf
                         ref[nb][c] = m;
-                        (c == 0 ? neg[nb].x : neg[nb].y) = -m;
+                        (c == 0 ? neg[nb].x : neg[nb].y) = -(m + kShift);
                         top[nb][c] = (m + 8.f) * inv_scale;
                         (c == 0 ? sum[nb].x : sum[nb].y) *= f;
                         sumr[nb][c] *= f;
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                     pk.x = pack_bf16x2(a.x * inv, a.y * inv);
                     pk.y = pack_bf16x2(a.z * inv, a.w * inv);
                     *reinterpret_cast<uint2*>(p.o + (row0 + rr) * D + 4 * c4) = pk;
-                    if (c4 == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    if (c4 == 0) p.lse[row0 + rr] = lse_of(m, l);
                 } else {
                     *reinterpret_cast<float4*>(p.part + ((long long)slot * RB + rr) * D + 4 * c4) = a;
                     if (c4 == 0)
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NB>::kCtasPerSm) attend_kerne
                         fin[rr] = n;
                         if (last_level) {
                             fin[RB + rr] = l == 0.f ? 0.f : 1.f / lr;
-                            p.lse[row0 + rr] = l == 0.f ? -INFINITY : (n + log2f(l)) * 0.69314718055994531f;
+                            p.lse[row0 + rr] = lse_of(n, l);
                         } else {
                             fin[RB + rr] = lr;
                             fin[2 * RB + rr] = l;

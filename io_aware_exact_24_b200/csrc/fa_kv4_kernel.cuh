@@ -158,6 +158,23 @@ struct RowsParams {
     float* part_ml;                  // and per row the max, the sum of rounded P and of P: [3][128]
 };
 
+// ---------------------------------------------------------------- weights
+// Weights are 2^(score - ref - kShift), with ref the reference max of the row, which may lag by 8:
+// at most 2^-8, so that sums of n values V stay below 2^127 while n |V| stays below 2^135 (2^15
+// keys of 2^120, or any number of 2^105), and at least 2^-126, which is 2^-110 of the largest
+// (smaller ones count as zero; with a shift of 24 that would be 2^-102, which shows where all other
+// keys of a row are so far below one whose value is 0).  At the other end of the format, where
+// values are multiples of 2^-110, sums of 32 bits still tell 2^-149 apart, 2^-23 of that at a
+// weight of 2^-16.  The shift cancels in O; the sum of the weights gets it back for the LSE.
+constexpr float kShift = 16.f;
+constexpr float kUnshift = 65536.f;          // 2^kShift
+// A reference of about m that is exact with and without the shift added.
+__device__ __forceinline__ float reference(float m) { return (m + kShift) - kShift; }
+// Log-sum-exp of a row, from its reference and the sum of its weights.
+__device__ __forceinline__ float lse_of(float ref, float sum) {
+    return sum == 0.f ? -INFINITY : (ref + log2f(sum * kUnshift)) * 0.69314718055994531f;
+}
+
 // ---------------------------------------------------------------- codes to bf16
 // The code at bits 4i .. 4i+3 of each half of w, as the bf16 pair (c - 8) * s: bits 3..6 of
 // a bf16 with the exponent of 16 weigh 8, 4, 2, 1, so the code placed there reads 16 + c,

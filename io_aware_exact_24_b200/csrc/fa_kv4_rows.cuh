@@ -514,14 +514,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
             }
             const float t_max = mx * c;
-            const float m_cur = (t_max > m_prev + kRescaleThreshold) ? t_max : m_prev;
+            const float m_cur = (t_max > m_prev + kRescaleThreshold) ? reference(t_max) : m_prev;
             if (j + 1 < n_kv)
                 st_relaxed_shared_u64(mref_w + 8u * (uint32_t)(g * kBlockM + r), ((unsigned long long)(uint32_t)j << 32) | __float_as_uint(m_cur));
             if (m_cur != m_seen) {
                 lu *= ex2_approx(m_seen - m_cur);
                 m_seen = m_cur;
             }
-            const float mu = (m_cur == -INFINITY) ? 0.f : m_cur;
+            const float mu = (m_cur == -INFINITY) ? 0.f : m_cur + kShift;
             const int pb = j % C::kPBufs;
             if (j >= C::kPBufs) {
                 good = wait_bounded(bar_pv_done(pb), (uint32_t)(((j - C::kPBufs) / C::kPBufs) & 1), abort_flag, p.wait_limit);
@@ -530,7 +530,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     break;
                 }
             }
-            // (all on MUFU: the polynomial of the dense forward would lose a NaN)
+            // P rounds to bf16 (2^-8) for the tensor cores; O is divided by the sum of the rounded
+            // values.  (All on MUFU: the polynomial of the dense forward would lose a NaN.)
             float2 lu2 = make_float2(0.f, 0.f);
             const uint32_t taddr_p = tmem + lane_off + C::col_p(pb);
             exp_store_half<0, 0>(s, c, mu, taddr_p, lu2);
@@ -659,8 +660,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
             }
             if (g == 0 && row < p.rows.R)
-                p.lse[((size_t)b * p.H_kv + h) * (size_t)p.rows.R + row] =
-                    lu_row == 0.f ? -INFINITY : (m_fin + log2f(lu_row)) * 0.69314718055994531f;
+                p.lse[((size_t)b * p.H_kv + h) * (size_t)p.rows.R + row] = lse_of(m_fin, lu_row);
         }
         fence_proxy_async_smem();
         const bool any_bad = named_bar_or(kBarSoftmaxAll, kSoftmaxWarps * 32, !good);
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams 
     y.x = pack_bf16x2(x.acc[0] * inv, x.acc[1] * inv), y.y = pack_bf16x2(x.acc[2] * inv, x.acc[3] * inv);
     y.z = pack_bf16x2(x.acc[4] * inv, x.acc[5] * inv), y.w = pack_bf16x2(x.acc[6] * inv, x.acc[7] * inv);
     *reinterpret_cast<uint4*>(p.o + out * D + 8 * c8) = y;
-    if (c8 == 0) p.lse[out] = x.lu == 0.f ? -INFINITY : (x.m + log2f(x.lu)) * 0.69314718055994531f;
+    if (c8 == 0) p.lse[out] = lse_of(x.m, x.lu);
 }
 
 }  // namespace kv4

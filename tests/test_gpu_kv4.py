@@ -905,3 +905,47 @@ def test_a_wait_that_runs_out_leaves_nan_and_the_next_call_is_right(B, H, H_kv, 
     assert fa_selftest_kv4_timeout(q, *c.buffers, c.d_table, lens, None, o, lse, B, H, H_kv, 1, *c.sizes, 0.1, True, -1, ws, n,
                                    2) == FA_ERR_INVALID_ARG
     check(c, bits, key_lens, None, 0.1, True, -1, *want[:2], heads=[0, H - 1])
+
+
+# ---------------------------------------------------------------- the ends of the range of V
+
+@pytest.mark.parametrize("end", ["top", "bottom"])
+@pytest.mark.parametrize("H,H_kv,N", [(1, 1, 1), (2, 1, 3), (16, 16, 1), (12, 2, 2), (8, 1, 8), (32, 32, 150), (4, 1, 150)])
+@pytest.mark.parametrize("d,n", [(64, 700), (128, 3000)])
+def test_values_at_the_ends_of_the_format(H, H_kv, N, d, n, end):
+    """V up to 2^120, all keys alike or after a tile that leaves the reference max 7 octaves behind, and
+    V down to 2^-107: O stays within the derived bound.
+
+    At the bottom, sums keep multiples of 2^-149 at weights of at least 2^-16 for the largest, so besides
+    the relative bounds O moves by (n/16 + 40) 2^-149 / 2^-16, and by 2^-134 where it rounds to a
+    subnormal bf16 number."""
+    page, maxp = 32, -(-n // 32)
+    top = 2.0 ** 120 if end == "top" else 2.0 ** -107
+    for lag in (False, True):
+        def edit(k, v):
+            x = bf16_bits_to_f32(k).astype(np.float64) * 0.01
+            # scores of q = 1 are scale * sum of k: 0 for the first 128 keys, then 7 octaves above
+            x[..., 0] += np.where(np.arange(n) < 128, 0.0, 7.0 * np.log(2.0)) if lag else 0.0
+            k[:] = f32_to_bf16_bits(x.astype(np.float32))
+            y = bf16_bits_to_f32(v).astype(np.float64)
+            y = np.clip(y / 4.0, -1.0, 1.0) * top
+            y[..., 5], y[..., 40] = top, -top                # and channels where all values are alike
+            v[:] = f32_to_bf16_bits(y.astype(np.float32))
+        c = filled(1, H_kv, page, d, maxp, [n], 141 + lag, edit=edit)
+        q = np.ones((1, H, N, d))
+        bits = f32_to_bf16_bits(q.astype(np.float32))
+        o, lse, guards = run_kv4(c, to_device_bf16(bits), [n], None, 1.0, True, -1)
+        assert guards
+        o, lse = to_host_f64(o), lse.cpu().numpy().astype(np.float64)
+        assert np.isfinite(o).all() and np.isfinite(lse).all()
+        kk, vv, _ = c.positions(0, n)
+        assert np.abs(vv).max() == top and np.isfinite(vv).all()
+        seen = kv4.visible_keys(N, N, n, n, True, -1)
+        for h in sorted({0, H - 1}):
+            kh, vh = kk[h // (H // H_kv)], vv[h // (H // H_kv)]
+            ro, rl = kv4.attend(q[0, h], kh, vh, seen, 1.0)
+            eo, el = bounds(q[0, h], kh, vh, seen, 1.0, ro, rl)
+            if end == "bottom":
+                eo = eo + (n / 16 + 40) * 2.0 ** -133 + 2.0 ** -134
+            assert (np.abs(o[0, h] - ro) <= eo).all(), (lag, h, (np.abs(o[0, h] - ro) / eo).max())
+            assert (np.abs(lse[0, h] - rl) <= el).all()
