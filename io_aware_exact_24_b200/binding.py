@@ -24,7 +24,7 @@ FA_ERR_DEVICE_TIMEOUT = -6
 _LIB_NAME = "libfa_b200.so"
 _lock = threading.Lock()
 _lib = None
-_fast = None   # the marshalling module of the 4-bit cache entry points, once the library is loaded
+_fast = None   # the marshalling module of the 4-bit cache entry points, from the first of their calls on
 
 
 class FaError(RuntimeError):
@@ -43,7 +43,7 @@ def library_path() -> str:
 
 def load_library() -> ctypes.CDLL:
     """Load the compiled library (raises if it has not been built)."""
-    global _lib, _fast
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -119,14 +119,6 @@ def load_library() -> ctypes.CDLL:
             lib.fa_last_error.restype = ctypes.c_char_p
             lib.fa_version.argtypes = []
             lib.fa_version.restype = i32
-            try:
-                from . import _fastcall
-            except ImportError as e:
-                raise ImportError("the _fastcall module is missing: build it with `python -m io_aware_exact_24_b200.build`") from e
-            _fastcall.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)),
-                           _current_device)
-            _fast = _fastcall
             _lib = lib
     return _lib
 
@@ -305,8 +297,19 @@ def _current_device() -> int:
 
 
 def _marshaller():
-    if _fast is None:
-        load_library()
+    """The marshalling module (raises if it has not been built; no other entry point needs it)."""
+    global _fast
+    lib = load_library()
+    with _lock:
+        if _fast is None:
+            try:
+                from . import _fastcall
+            except ImportError as e:
+                raise ImportError("the 4-bit cache calls need the _fastcall module: build it with "
+                                  "`python -m io_aware_exact_24_b200.build` (gcc and Python's headers)") from e
+            _fastcall.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)), _current_device)
+            _fast = _fastcall
     return _fast
 
 

@@ -46,7 +46,18 @@ def build_fastcall(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_fastcall(force)
+    """The library, and the marshalling module, without which only the 4-bit cache calls cannot be made."""
+    out = build_library(force, verbose)
+    try:
+        build_fastcall(force)
+    except (OSError, subprocess.CalledProcessError) as e:
+        if os.path.exists(FAST_OUT):
+            os.remove(FAST_OUT)   # of other sources
+        print(f"the 4-bit cache calls are not available from Python: {e}", file=sys.stderr)
+    return out
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(OUT):
         t = os.path.getmtime(OUT)
         if all(os.path.getmtime(f) <= t for f in DEPENDS):

@@ -119,8 +119,8 @@ def test_the_arithmetic_of_the_codes_gives_the_format():
     # what the kernels compute, each step rounded to bf16: t = 1024 s, z = t - 131/128 t (-24 s, or
     # NaN from |s| = 2^118 on, where t is infinite), and (16 + c) s + z
     bits = np.arange(1 << 16, dtype=np.uint16)
-    s = bf16_bits_to_f32(bits).astype(np.float64)
     with np.errstate(all="ignore"):
+        s = bf16_bits_to_f32(bits).astype(np.float64)
         t = bf16_round(s * 1024.0)
         z = bf16_round(t * (-131.0 / 128.0) + t)
         got = [bf16_round((16.0 + c) * s + z) for c in range(16)]
@@ -320,6 +320,41 @@ def test_tensors_elsewhere_are_refused(lib):
             call(B=0, **{kw: Elsewhere(here + 1, True)})
         with pytest.raises(ValueError, match="contiguous"):
             call(B=0, **{kw: Elsewhere(here, False)})
+
+
+def test_other_entry_points_do_without_the_marshalling_module(lib):
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.modules["io_aware_exact_24_b200._fastcall"] = None          # as if it had not been built
+import io_aware_exact_24_b200 as fa
+P = 1 << 20
+assert fa.fa_fwd(P, P, P, P, P, 0, 1, 8, 8, 64, 0.125, 0, None, 0) == fa.FA_OK
+assert fa.binding.fa_fwd(P, P, P, P, P, 1, 1, 8, 8, 96, 0.125, 0, None, 0, False) == fa.FA_ERR_UNSUPPORTED
+assert fa.fa_fwd_kv4_workspace_size(1, 1, 1, 1, 64) > 0
+for _ in range(2):
+    try:
+        fa.fa_kv4_append(P, P, P, P, P, P, P, P, P, 0, 1, 1, 64, 4, 16, 4, 0)
+    except ImportError as e:
+        assert "_fastcall" in str(e)
+    else:
+        raise AssertionError("no error")
+"""
+    root = os.path.dirname(os.path.dirname(binding.__file__))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
+
+
+def test_the_library_is_built_where_the_marshalling_module_cannot_be(tmp_path, monkeypatch, capfd):
+    from io_aware_exact_24_b200 import build as module
+    monkeypatch.setattr(module, "FAST_OUT", str(tmp_path / "_fastcall.so"))
+    for cc in ("false", str(tmp_path / "no_such_compiler")):
+        (tmp_path / "_fastcall.so").write_text("of older sources")
+        os.utime(tmp_path / "_fastcall.so", (1, 1))
+        monkeypatch.setenv("CC", cc)
+        assert module.build() == module.OUT
+        assert "4-bit cache calls are not available" in capfd.readouterr().err
+        assert not (tmp_path / "_fastcall.so").exists()
 
 
 def test_workspace_size(lib):
