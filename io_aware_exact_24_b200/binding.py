@@ -296,6 +296,12 @@ def _current_device() -> int:
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
+def _tensor_types():
+    """The types of the 4-bit cache's tensors, in the order of fa_fastcall.c."""
+    import torch
+    return torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _marshaller():
     """The marshalling module (raises if it has not been built; no other entry point needs it)."""
     global _fast
@@ -308,7 +314,7 @@ def _marshaller():
                 raise ImportError("the 4-bit cache calls need the _fastcall module: build it with "
                                   "`python -m io_aware_exact_24_b200.build` (gcc and Python's headers)") from e
             _fastcall.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)), _current_device)
+                             for f in (lib.fa_kv4_append, lib.fa_kv4_read, lib.fa_fwd_kv4)), _current_device, _tensor_types)
             _fast = _fastcall
     return _fast
 

@@ -5,8 +5,11 @@
  * microseconds, as long as the kernels of a small step run.  The wrappers here take the same
  * arguments as those of binding.py and turn them into the same C calls: tensors (anything with
  * data_ptr()), integers and None become addresses, numbers become numbers.  They compute
- * nothing and link against nothing; init() hands them the entry points' addresses.  Of the
- * tensors, the dense ones must be contiguous, and they and the cache on the current device.
+ * nothing and link against nothing; init() hands them the entry points' addresses.  Tensors
+ * must be contiguous, on the current device and of the argument's type: the kernels would read
+ * other memory than they mean, or fault.  (Of a call that does nothing, B, heads or tokens 0,
+ * only the dense ones and a buffer of the cache are looked at.)  Addresses are taken as they are.
+ * That is 0.3 us of the 5.9 that an attention call takes the host, its launch included.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -21,8 +24,23 @@ typedef int (*fwd_fn)(const void *, const void *, const void *, const void *, co
 
 static rows_fn g_append, g_read;
 static fwd_fn g_fwd;
-static PyObject *g_data_ptr, *g_get_device, *g_is_contiguous;   /* names of a tensor's methods */
+static PyObject *g_data_ptr, *g_get_device, *g_is_contiguous, *g_dtype;   /* names of a tensor's methods and its type's */
 static PyObject *g_current;                                     /* returns the current device */
+static PyObject *g_make_types;                                  /* returns a tuple of the types below */
+static PyObject *g_types;                                       /* it, from the first tensor on */
+
+enum type { BF16, F32, I32, U8, ANY };
+struct arg {
+    const char *name;
+    enum type type;
+};
+static const struct arg append_args[9] = {{"k", BF16}, {"v", BF16}, {"k_codes", U8}, {"k_scales", BF16}, {"v_codes", U8},
+                                          {"v_scales", BF16}, {"block_table", I32}, {"key_lens", I32}, {"new_lens", I32}};
+static const struct arg read_args[9] = {{"k_codes", U8}, {"k_scales", BF16}, {"v_codes", U8}, {"v_scales", BF16},
+                                        {"block_table", I32}, {"key_lens", I32}, {"first", I32}, {"k", BF16}, {"v", BF16}};
+static const struct arg fwd_args[10] = {{"q", BF16}, {"k_codes", U8}, {"k_scales", BF16}, {"v_codes", U8}, {"v_scales", BF16},
+                                        {"block_table", I32}, {"key_lens", I32}, {"q_lens", I32}, {"o", BF16}, {"lse", F32}};
+static const struct arg workspace_arg = {"workspace", ANY};
 
 static int not_a_tensor(PyObject *x) {
     if (PyErr_ExceptionMatches(PyExc_AttributeError)) {
@@ -49,35 +67,58 @@ static int address(PyObject *x, void **out) {
     return *out != NULL || !PyErr_Occurred() ? -1 : 0;
 }
 
-/* A tensor given here must lie on the current device, and, where asked, be contiguous: the
- * kernels would read other memory than it means, or fault.  Addresses are taken as they are. */
-static int tensor_ok(PyObject *x, int contiguous) {
+static int current_device(long *dev) {
+    PyObject *c = PyObject_CallNoArgs(g_current);
+    if (c == NULL) return 0;
+    *dev = PyLong_AsLong(c);
+    Py_DECREF(c);
+    return *dev != -1 || !PyErr_Occurred() ? -1 : 0;
+}
+
+static int tensor_on(PyObject *x, const struct arg *arg, long current) {
     if (x == Py_None || PyLong_Check(x)) return -1;
     PyObject *d = PyObject_CallMethodNoArgs(x, g_get_device);
     if (d == NULL) return not_a_tensor(x);
     const long dev = PyLong_AsLong(d);
     Py_DECREF(d);
-    PyObject *c = PyObject_CallNoArgs(g_current);
-    if (c == NULL) return 0;
-    const long cur = PyLong_AsLong(c);
-    Py_DECREF(c);
-    if (PyErr_Occurred()) return 0;
-    if (dev != cur) {
-        PyErr_Format(PyExc_ValueError, "a tensor is on device %ld, the current device is %ld (-1: the CPU)", dev, cur);
-        return 0;
-    }
-    if (contiguous) {
-        PyObject *r = PyObject_CallMethodNoArgs(x, g_is_contiguous);
-        if (r == NULL) return 0;
-        const int yes = PyObject_IsTrue(r);
-        Py_DECREF(r);
-        if (yes < 0) return 0;
-        if (!yes) {
-            PyErr_SetString(PyExc_ValueError, "a tensor is not contiguous");
+    if (dev == -1 && PyErr_Occurred()) return 0;
+    if (dev == current) return -1;
+    PyErr_Format(PyExc_ValueError, "%s is on device %ld, the current device is %ld (-1: the CPU)", arg->name, dev, current);
+    return 0;
+}
+
+static int tensor_contiguous(PyObject *x, const struct arg *arg) {
+    if (x == Py_None || PyLong_Check(x)) return -1;
+    PyObject *r = PyObject_CallMethodNoArgs(x, g_is_contiguous);
+    if (r == NULL) return not_a_tensor(x);
+    const int yes = PyObject_IsTrue(r);
+    Py_DECREF(r);
+    if (yes > 0) return -1;
+    if (yes == 0) PyErr_Format(PyExc_ValueError, "%s is not contiguous", arg->name);
+    return 0;
+}
+
+static int tensor_type(PyObject *x, const struct arg *arg) {
+    if (x == Py_None || PyLong_Check(x) || arg->type == ANY) return -1;
+    if (g_types == NULL) {
+        g_types = PyObject_CallNoArgs(g_make_types);
+        if (g_types == NULL) return 0;
+        if (!PyTuple_Check(g_types) || PyTuple_GET_SIZE(g_types) != ANY) {
+            Py_CLEAR(g_types);
+            PyErr_SetString(PyExc_SystemError, "a tuple of types was expected");
             return 0;
         }
     }
-    return -1;
+    PyObject *want = PyTuple_GET_ITEM(g_types, arg->type), *t = PyObject_GetAttr(x, g_dtype);
+    if (t == NULL) return not_a_tensor(x);
+    const int same = t == want;                  /* (each type is one object) */
+    if (!same) PyErr_Format(PyExc_ValueError, "%s is of type %R, %R expected", arg->name, t, want);
+    Py_DECREF(t);
+    return same ? -1 : 0;
+}
+
+static int tensor_ok(PyObject *x, const struct arg *arg, long current) {
+    return tensor_on(x, arg, current) && tensor_contiguous(x, arg) && tensor_type(x, arg) ? -1 : 0;
 }
 
 static int number(PyObject *x, int *out) {
@@ -101,15 +142,20 @@ static int count_is(Py_ssize_t n, Py_ssize_t want) {
 }
 
 /* 9 addresses, 7 numbers, the stream; a[dense] and a[dense + 1] are k and v, a[cache] a buffer of the cache */
-static PyObject *rows_call(rows_fn fn, PyObject *const *a, Py_ssize_t n, int dense, int cache) {
+static PyObject *rows_call(rows_fn fn, const struct arg *args, PyObject *const *a, Py_ssize_t n, int dense, int cache) {
     void *p[9], *stream;
     int v[7], i;
-    if (!count_is(n, 17)) return NULL;
-    if (!tensor_ok(a[dense], 1) || !tensor_ok(a[dense + 1], 1) || !tensor_ok(a[cache], 0)) return NULL;
-    for (i = 0; i < 9; ++i)
-        if (!address(a[i], &p[i])) return NULL;
+    long dev;
+    if (!count_is(n, 17) || !current_device(&dev)) return NULL;
     for (i = 0; i < 7; ++i)
         if (!number(a[9 + i], &v[i])) return NULL;
+    const int nothing = v[0] == 0 || v[1] == 0 || v[2] == 0;
+    for (i = 0; i < 9; ++i) {
+        const int is_dense = i == dense || i == dense + 1;
+        if (nothing ? (is_dense || i == cache) && !tensor_on(a[i], &args[i], dev) : !tensor_ok(a[i], &args[i], dev)) return NULL;
+        if (nothing && is_dense && !tensor_contiguous(a[i], &args[i])) return NULL;
+        if (!address(a[i], &p[i])) return NULL;
+    }
     if (!address(a[16], &stream)) return NULL;
     int st;
     Py_BEGIN_ALLOW_THREADS
@@ -118,19 +164,25 @@ static PyObject *rows_call(rows_fn fn, PyObject *const *a, Py_ssize_t n, int den
     return PyLong_FromLong(st);
 }
 
-static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_append, a, n, 0, 2); }
-static PyObject *read_back(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_read, a, n, 7, 0); }
+static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_append, append_args, a, n, 0, 2); }
+static PyObject *read_back(PyObject *self, PyObject *const *a, Py_ssize_t n) { return rows_call(g_read, read_args, a, n, 7, 0); }
 
 /* 10 addresses, 8 numbers, scale, causal, window, workspace and its size, the stream */
 static PyObject *fwd(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *p[10], *ws, *stream;
     int v[8], window, i;
-    if (!count_is(n, 24)) return NULL;
-    if (!tensor_ok(a[0], 1) || !tensor_ok(a[8], 1) || !tensor_ok(a[1], 0)) return NULL;   /* q, o, the cache */
-    for (i = 0; i < 10; ++i)
-        if (!address(a[i], &p[i])) return NULL;
+    long dev;
+    if (!count_is(n, 24) || !current_device(&dev)) return NULL;
     for (i = 0; i < 8; ++i)
         if (!number(a[10 + i], &v[i])) return NULL;
+    const int nothing = v[0] == 0 || v[1] == 0 || v[2] == 0 || v[3] == 0;
+    for (i = 0; i < 10; ++i) {
+        const int is_dense = i == 0 || i == 8;   /* q and o */
+        if (nothing ? (is_dense || i == 1) && !tensor_on(a[i], &fwd_args[i], dev) : !tensor_ok(a[i], &fwd_args[i], dev)) return NULL;
+        if (nothing && is_dense && !tensor_contiguous(a[i], &fwd_args[i])) return NULL;
+        if (!address(a[i], &p[i])) return NULL;
+    }
+    if (!nothing && !tensor_ok(a[21], &workspace_arg, dev)) return NULL;
     const double scale = PyFloat_AsDouble(a[18]);
     if (scale == -1.0 && PyErr_Occurred()) return NULL;
     const int causal = PyObject_IsTrue(a[19]);
@@ -152,9 +204,11 @@ static PyObject *fwd(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyObject *init(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *p[3];
     int i;
-    if (!count_is(n, 4)) return NULL;
+    if (!count_is(n, 5)) return NULL;
     Py_INCREF(a[3]);
     Py_XSETREF(g_current, a[3]);
+    Py_INCREF(a[4]);
+    Py_XSETREF(g_make_types, a[4]);
     for (i = 0; i < 3; ++i)
         if (!address(a[i], &p[i])) return NULL;
     g_append = (rows_fn)p[0];
@@ -164,7 +218,7 @@ static PyObject *init(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 static PyMethodDef methods[] = {
-    {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, "init(fa_kv4_append, fa_kv4_read, fa_fwd_kv4, current_device): their addresses, and a function"},
+    {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, "init(fa_kv4_append, fa_kv4_read, fa_fwd_kv4, current_device, types): their addresses, and two functions"},
     {"fa_kv4_append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "status of fa_kv4_append"},
     {"fa_kv4_read", (PyCFunction)(void (*)(void))read_back, METH_FASTCALL, "status of fa_kv4_read"},
     {"fa_fwd_kv4", (PyCFunction)(void (*)(void))fwd, METH_FASTCALL, "status of fa_fwd_kv4"},
@@ -177,6 +231,7 @@ PyMODINIT_FUNC PyInit__fastcall(void) {
     g_data_ptr = PyUnicode_InternFromString("data_ptr");
     g_get_device = PyUnicode_InternFromString("get_device");
     g_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    if (g_data_ptr == NULL || g_get_device == NULL || g_is_contiguous == NULL) return NULL;
+    g_dtype = PyUnicode_InternFromString("dtype");
+    if (g_data_ptr == NULL || g_get_device == NULL || g_is_contiguous == NULL || g_dtype == NULL) return NULL;
     return PyModule_Create(&module);
 }

@@ -949,3 +949,50 @@ def test_values_at_the_ends_of_the_format(H, H_kv, N, d, n, end):
                 eo = eo + (n / 16 + 40) * 2.0 ** -133 + 2.0 ** -134
             assert (np.abs(o[0, h] - ro) <= eo).all(), (lag, h, (np.abs(o[0, h] - ro) / eo).max())
             assert (np.abs(lse[0, h] - rl) <= el).all()
+
+
+# ---------------------------------------------------------------- tensors that do not fit
+
+def test_tensors_that_do_not_fit_are_refused_and_nothing_is_touched():
+    """int64 lengths, a slice of a wider table, one tensor for codes of K and V, tensors on the CPU."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
+    B, H, H_kv, N, d, page, maxp, num = 2, 2, 2, 3, 64, 16, 2, 8
+    k = torch.zeros((B, H_kv, N, d), dtype=torch.bfloat16, device="cuda")
+    kb, q, o = k.clone(), k.clone(), k.clone()
+    lse = torch.zeros((B, H, N), device="cuda")
+    codes = torch.full((num, H_kv, page, d // 2), 7, dtype=torch.uint8, device="cuda")
+    scales = torch.full((num, H_kv, page, d // 32), 7.0, dtype=torch.bfloat16, device="cuda")
+    size = fa_fwd_kv4_workspace_size(B, H, H_kv, N, d)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    good = dict(kc=codes, ks=scales, vc=codes.clone(), vs=scales.clone(), table=ints([[0, 1], [2, 3]]), lens=ints([3, 3]),
+                new=ints([3, 3]), k=k, v=k.clone(), q=q, o=o, lse=lse, ws=ws)
+    keep = {n: t.clone() for n, t in good.items()}
+
+    def calls(**kw):
+        a = good | kw
+        cache = (a["kc"], a["ks"], a["vc"], a["vs"], a["table"], a["lens"])
+        sizes = (d, num, page, maxp)
+        return (lambda: fa_kv4_append(a["k"], a["v"], *cache, a["new"], B, H_kv, N, *sizes),
+                lambda: fa_kv4_read(*cache, a["new"], a["k"], a["v"], B, H_kv, N, *sizes),
+                lambda: fa_fwd_kv4(a["q"], *cache, a["new"], a["o"], a["lse"], B, H, H_kv, N, *sizes, 0.1, True, -1, a["ws"], size))
+    wide = ints([[0, 1, 9, 9], [2, 3, 9, 9]])
+    both = torch.zeros((num, H_kv, page, 2, d // 2), dtype=torch.uint8, device="cuda")
+    every, attend = (0, 1, 2), (2,)
+    for kw, which in ((dict(lens=ints([3, 3], np.int64)), every), (dict(new=ints([3, 3], np.int64)), every),
+                      (dict(table=ints([[0, 1], [2, 3]], np.int64)), every), (dict(table=wide[:, :2]), every),
+                      (dict(lens=ints([3, 3, 3, 3])[::2]), every), (dict(kc=both[..., 0, :], vc=both[..., 1, :]), every),
+                      (dict(ks=scales.half()), every), (dict(vs=scales.float()), every), (dict(lens=ints([3, 3]).cpu()), every),
+                      (dict(table=good["table"].cpu()), every), (dict(vc=codes.cpu()), every), (dict(k=k.half()), (0, 1)),
+                      (dict(q=q.transpose(1, 2)), attend), (dict(lse=lse.double()), attend), (dict(lse=lse.cpu()), attend),
+                      (dict(ws=ws.cpu()), attend), (dict(ws=torch.zeros(2 * size, dtype=torch.uint8, device="cuda")[::2]), attend)):
+        for i in which:
+            with pytest.raises(ValueError):
+                calls(**kw)[i]()
+    torch.cuda.synchronize()
+    for n, t in good.items():
+        assert torch.equal(t, keep[n]), n
+    for call in calls():
+        call()
+    torch.cuda.synchronize()
+    assert not torch.equal(codes, keep["kc"])

@@ -357,6 +357,48 @@ def test_the_library_is_built_where_the_marshalling_module_cannot_be(tmp_path, m
         assert not (tmp_path / "_fastcall.so").exists()
 
 
+TYPES = dict(k="bfloat16", v="bfloat16", q="bfloat16", o="bfloat16", lse="float32", kc="uint8", vc="uint8", ks="bfloat16",
+             vs="bfloat16", table="int32", key_lens="int32", lens="int32", ws=None)
+
+
+class Tensor:
+    """What the marshalling looks at."""
+
+    def __init__(self, dtype, device=0, contiguous=True):
+        self.dtype, self.device, self.contiguous = dtype, device, contiguous
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return P
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in ((append, "k v"), (read, "k v"), (fwd, "q o lse ws"))
+                                       for n in (names + " kc ks vc vs table key_lens lens").split()])
+def test_every_tensor_is_looked_at(lib, call, name):
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else 0
+    dtype = getattr(torch, TYPES[name] or "uint8")
+    # d = 96 is refused by the library, so that nothing is launched where all is well
+    assert call(d=96, **{name: Tensor(dtype, here)}) == UNSUPPORTED
+    with pytest.raises(ValueError, match="device"):
+        call(d=96, **{name: torch.zeros(64, dtype=dtype)})                     # on the CPU
+    with pytest.raises(ValueError, match="device"):
+        call(d=96, **{name: Tensor(dtype, here + 1)})
+    with pytest.raises(ValueError, match="contiguous"):
+        call(d=96, **{name: Tensor(dtype, here, False)})
+    for other in (torch.int64, torch.float16, torch.float32, torch.bfloat16, torch.int32, torch.uint8):
+        if other != dtype and TYPES[name] is not None:
+            with pytest.raises(ValueError, match="expected"):
+                call(d=96, **{name: Tensor(other, here)})
+    with pytest.raises(TypeError):
+        call(d=96, **{name: "x"})
+
+
 def test_workspace_size(lib):
     n = binding.fa_fwd_kv4_workspace_size(3, 8, 2, 1, 128)
     assert n > 0 and n % 256 == 0
