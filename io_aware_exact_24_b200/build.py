@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_kv4.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fwd_persist.cuh", "fa_decode_kernel.cuh", "fa_bwd_kernel.cuh", "sm100_ptx.cuh",
                                                      "exp2_poly.cuh", "fa_kv4_kernel.cuh", "fa_kv4_attend.cuh", "fa_kv4_rows.cuh",
-                                                     "fa_internal.h")] + [
+                                                     "fa_internal.h", "fa_kv4_rule.h")] + [
     os.path.join(ROOT, "include", "fa.h")]
 OUT = os.path.join(PKG, "libfa_b200.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

@@ -13,6 +13,7 @@
 #include "fa_internal.h"
 #include "fa_kv4_attend.cuh"
 #include "fa_kv4_kernel.cuh"
+#include "fa_kv4_rule.h"
 
 namespace {
 
@@ -81,52 +82,11 @@ unsigned long long next_ticket() {
     return t;
 }
 
-int ctas_per_sm(int rb) { return rb == 8 ? kv4::Cfg<128, 1>::kCtasPerSm : kv4::Cfg<128, 2>::kCtasPerSm; }
-
-// Time of the kernel for few rows, in us, for sequences of up to `keys` keys and rb rows a block.
-// One MMA column block holds 8 query rows: 0.62 us of an SM for 128 keys; two share a
-// dequantised operand, at 0.84, but leave two CTAs to an SM instead of three and start later.
-// Each part of an item adds to its merge, of 8 rows up to two levels' (fa_kv4_attend.cuh).
-double few_rows_us(long long R, long long heads, int rb, long long keys, int num_sms) {
-    const long long items = (R + rb - 1) / rb * heads;
-    const double units = (double)items * (double)keys / kv4::kUnit;
-    const double parts = std::min((double)keys / kv4::kUnit, (double)num_sms * ctas_per_sm(rb) / (double)items);
-    return rb == 8 ? 9. + .62 * units / num_sms + std::min(5., .1 * parts) : 12.5 + .84 * units / num_sms + .2 * parts;
-}
-
-// Rows per block, 8 or 16: the quicker one.  Measured, in us, 8 and 16 (16 rows):
-//      8 heads    700 keys  9.8, 12.9     8192 keys 19.4, 25.1     65536 keys 48.2, 46.1
-//     64 heads    700 keys 12.8, 15.3     2048 keys 21.3, 23.6      4096 keys 30.6, 29.7
-//     16 heads  32768 keys 47.2, 41.5;  2 heads, 131072 keys 33.6, 55.9
-int row_block(long long R, long long heads, long long keys, int num_sms) {
-    return R <= 8 || few_rows_us(R, heads, 8, keys, num_sms) <= few_rows_us(R, heads, 16, keys, num_sms) ? 8 : 16;
-}
-
-// CTAs of the kernel for many rows (fa_kv4_rows.cuh) that share the keys of a block of rows,
-// where the blocks alone would leave half the SMs idle: at most as many as fill the SMs once,
-// each with two tiles or more of the longest sequence there could be.  8 heads of 32768 keys,
-// 128 rows: one CTA a block about 340 us, 18 of them 32; 1024 rows, two CTAs, 173.
-int most_splits(long long R, long long heads, int num_sms) {
-    return (int)std::max<long long>(1, num_sms / ((R + 127) / 128 * heads));
-}
-int key_splits(long long R, long long heads, int num_sms, long long keys) {
-    return (int)std::max<long long>(1, std::min<long long>(most_splits(R, heads, num_sms), keys / 256));
-}
-
-// Whether the kernel for many rows is the quicker one: each wave of its CTAs takes about 3 us and
-// 1.3 for each tile of 128 keys.  Measured, in us, many rows and few:
-//     8 heads,   700 keys     20 rows 11.3,  9.8     64 rows 11.9, 10.5     256 rows 13.7,  16.5
-//     8 heads,  8192 keys     20 rows 16.6, 19.8     64 rows 17.0, 28.8    1024 rows 56.8, 173
-//    64 heads,  4096 keys     20 rows 34.5, 38.3     64 rows 34.6, 57.7     256 rows 50.7, 184
-//    64 heads, window 2048    20 rows 25.3, 27.1     64 rows 26.8, 40.0     256 rows 31.9, 117
-//   512 heads,   700 keys (d = 64)   20 rows 49.7, 37.9     64 rows 49.6, 73.6
-bool many_rows(long long R, long long heads, int splits, int num_sms, long long keys) {
-    if (R <= 16) return false;
-    const long long tiles = (keys + 127) / 128, waves = ((R + 127) / 128 * heads * splits + num_sms - 1) / num_sms;
-    const double many = (splits > 1 ? 7. : 5.) + (double)waves * (3. + 1.3 * (double)((tiles + splits - 1) / splits));
-    const double few = few_rows_us(R, heads, row_block(R, heads, keys, num_sms), keys, num_sms);
-    return many < few;
-}
+using kv4::ctas_per_sm;
+static_assert(ctas_per_sm(8) == kv4::Cfg<128, 1>::kCtasPerSm && ctas_per_sm(8) == kv4::Cfg<64, 1>::kCtasPerSm &&
+                  ctas_per_sm(16) == kv4::Cfg<128, 2>::kCtasPerSm && ctas_per_sm(16) == kv4::Cfg<64, 2>::kCtasPerSm &&
+                  kv4::kRuleUnit == kv4::kUnit && kv4::kRuleEntries == kv4::kMaxEntries,
+              "the rule's kernels");
 
 // Workspace of the attention: two partial results per CTA, then the arrival words.  The kernel
 // for many rows keeps one partial result per CTA where it splits the keys.
@@ -143,7 +103,7 @@ Layout layout(int B, int H, int H_kv, int N_q, int d, int num_sms, int rb) {
     L.words = L.ml + round_up(slots * rb * 16);
     L.group_words = L.words + round_up((size_t)std::min<long long>(entries, kv4::kMaxEntries) * H_kv * 8);
     L.total = L.group_words + round_up(slots * 8);
-    const int splits = R > 16 ? most_splits(R, (long long)B * H_kv, num_sms) : 1;
+    const int splits = R > 16 ? kv4::most_splits(R, (long long)B * H_kv, num_sms) : 1;
     if (splits > 1) {
         const size_t parts = (size_t)splits * B * H_kv * ((R + 127) / 128) * 128;   // rows
         L.rows_ml = round_up(parts * d * 4);
@@ -230,14 +190,13 @@ int fwd(const void* q, const void* k_codes, const void* k_scales, const void* v_
     rows.window = window_left < 0 ? -1 : std::min(window_left, kMaxPositions);
     const kv4::Paging pg = paging(block_table, num_pages, page_size, max_pages);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    long long keys = (long long)max_pages * page_size;
-    if (window_left >= 0) keys = std::min(keys, (long long)rows.window + N_q);
-    const int rb = row_block(R, (long long)B * H_kv, keys, sms);
+    const long long room = (long long)max_pages * page_size;
+    const kv4::Choice choice = kv4::choose(B, H_kv, R, N_q, d, room, rows.window, sms);
+    const int rb = choice.rows_a_block;
+    const long long keys = kv4::block_keys(room, rows.window, N_q, rb);
     const Layout L = layout(B, H, H_kv, N_q, d, sms, rb);
-    const int splits = key_splits(R, (long long)B * H_kv, sms, keys);
-    const bool many = many_rows(R, (long long)B * H_kv, splits, sms, keys);
-    if (wait_limit > 0 && !many) return FA_ERR_INVALID_ARG;   // nothing would wait
-    if (many) {
+    if (wait_limit > 0 && !choice.many) return FA_ERR_INVALID_ARG;   // nothing would wait
+    if (choice.many) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         kv4::RowsParams p{};
         p.k_codes = static_cast<const uint8_t*>(k_codes);
@@ -250,7 +209,7 @@ int fwd(const void* q, const void* k_codes, const void* k_scales, const void* v_
         p.o = static_cast<__nv_bfloat16*>(o);
         p.lse = lse;
         p.scale_log2 = scale_log2;
-        p.splits = splits;
+        p.splits = choice.splits;
         p.wait_limit = wait_limit;
         p.part = reinterpret_cast<float*>(ws);
         p.part_ml = reinterpret_cast<float*>(ws + L.rows_ml);

@@ -9,6 +9,17 @@ TOL_REL_FROB_O = 4e-3
 TOL_ABS_LSE = 1e-3
 
 
+# Calls of the 4-bit cache attention that take blocks of 16 rows:
+# B, H, H_kv, N_q, d, page_size, max_pages, window
+SIXTEEN_ROWS = [
+    (300, 3, 1, 4, 128, 16, 20, 100),
+    (300, 3, 1, 4, 64, 48, 5, 20),
+    (300, 1, 1, 12, 128, 64, 5, -1),
+    (300, 1, 1, 12, 64, 32, 4, 100),
+    (300, 2, 1, 8, 128, 128, 3, 200),
+]
+
+
 def to_device_bf16(bits, device="cuda"):
     import torch
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).to(device).view(torch.bfloat16)

@@ -8,7 +8,7 @@ import pytest
 import oracle.kv4 as kv4
 from io_aware_exact_24_b200.inputs import bf16_bits_to_f32, f32_to_bf16_bits, normal_bf16
 
-from fa_testutil import run_fa, to_device_bf16, to_host_f64
+from fa_testutil import SIXTEEN_ROWS, run_fa, to_device_bf16, to_host_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -996,3 +996,39 @@ def test_tensors_that_do_not_fit_are_refused_and_nothing_is_touched():
         call()
     torch.cuda.synchronize()
     assert not torch.equal(codes, keep["kc"])
+
+
+# ---------------------------------------------------------------- sixteen rows a block
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,window", SIXTEEN_ROWS)
+def test_sixteen_rows_a_block(B, H, H_kv, N, d, page, maxp, window):
+    """Ragged lengths and queries, windows, foreign scales in rows that no query sees, missing pages."""
+    import torch
+    top = page * maxp
+    key_lens = [top if b == 0 else (53 * b) % top for b in range(B)]
+    q_lens = [N if b % 3 else b % (N + 1) for b in range(B)]
+    table = np.random.default_rng(151).permutation(B * maxp).reshape(B, maxp)
+    c = Cache(B * maxp, H_kv, page, d, maxp, table)
+    (k, v), _ = tokens(B, H_kv, top, d, 152)
+    c.append(k, v, [top] * B)
+    bits = normal_bf16((B, H, N, d), 153, 0)
+    q = to_device_bf16(bits)
+    for causal in (True, False):
+        o, lse, guards = run_kv4(c, q, key_lens, q_lens, 0.1, causal, window)
+        assert guards
+        check(c, bits, key_lens, q_lens, 0.1, causal, window, o, lse, heads=[0, H - 1], what=str(causal))
+    # rows behind the lengths, and those that all windows leave out, hold what was never written
+    want = run_kv4(c, q, key_lens, None, 0.1, True, window)
+    for scale in (0x7D80, 0xFF80, 0x7FC0):
+        for b in range(0, B, max(1, B // 7)):
+            for j in range(top):
+                if j >= key_lens[b] or (window >= 0 and j < key_lens[b] - N - window):
+                    for s in (c.k_scales, c.v_scales):
+                        s[int(table[b][j // page]), :, j % page] = bf16_of([scale])[0]
+        o, lse, _ = run_kv4(c, q, key_lens, None, 0.1, True, window)
+        assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1]), hex(scale)
+    table[:, 1::3] = -1
+    c.table[...] = table
+    c.d_table.copy_(ints(table))
+    o, lse, _ = run_kv4(c, q, key_lens, None, 0.1, True, window)
+    check(c, bits, key_lens, None, 0.1, True, window, o, lse, heads=[0, H - 1], what="missing pages")

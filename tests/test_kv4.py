@@ -11,6 +11,8 @@ from io_aware_exact_24_b200 import binding
 from io_aware_exact_24_b200.build import build
 from io_aware_exact_24_b200.inputs import bf16_bits_to_f32, f32_to_bf16_bits, normal_bf16
 
+from fa_testutil import SIXTEEN_ROWS
+
 
 @pytest.fixture(scope="module")
 def lib():
@@ -172,6 +174,105 @@ def test_kernels_that_overlap_the_one_before_load_nothing_as_read_only():
             body = code[code.index(kernel + "("):]
             before = body[:body.index("after_previous();")]
             assert not re.search(r"p\.(q|k|v|o|lse|part|part_ml|words|key_lens|\w+_codes|\w+_scales)\b|tma_load|cp_async16", before), kernel
+
+
+# ---------------------------------------------------------------- the choice of a kernel
+
+# B, H_kv, rows a head (the queries), keys, d, window, and us measured on one B200 of the kernel for
+# few rows with 8 and with 16 rows a block, and of the one for many rows
+MEASURED = [
+    (8, 8, 20, 16, 128, -1, 6.1, 8.1, 8.1),
+    (8, 8, 512, 16, 128, -1, 40.3, 42.6, 17),
+    (64, 32, 20, 16, 128, -1, 56.2, 81.2, 106.4),
+    (64, 32, 512, 1, 128, -1, 1190.6, 1336.7, 441.8),
+    (64, 32, 200, 16, 64, -1, 367.6, 381.3, 202.5),
+    (8, 8, 4096, 64, 128, -1, 327.9, 314.5, 115.8),
+    (8, 8, 4096, 64, 64, -1, 252.2, 211.8, 103.7),
+    (256, 1, 64, 64, 128, -1, 45.1, 29.2, 16.7),
+    (8, 32, 200, 1, 128, -1, 58.3, 69.5, 31.7),
+    (8, 32, 9, 128, 128, -1, 9.9, 7.7, 14.8),
+    (100, 1, 300, 60, 128, -1, 95.8, 65.7, 22.3),
+    (100, 1, 700, 5, 64, -1, 180.6, 113.3, 33.5),
+    (100, 1, 24, 60, 128, -1, 8.9, 10.2, 8.8),
+    (125, 8, 100, 60, 128, -1, 149.4, 158.1, 58.6),
+    (125, 8, 40, 60, 64, -1, 45.1, 47.5, 50.5),
+    (75, 2, 300, 260, 128, -1, 155.9, 133.2, 40.9),
+    (37, 4, 10, 260, 64, -1, 15.8, 18.8, 11),
+    (1, 8, 20, 700, 128, -1, 10.2, 13.1, 12.2),
+    (1, 8, 256, 700, 128, -1, 19.3, 16.6, 14.3),
+    (8, 8, 20, 700, 128, -1, 13.7, 16.3, 16.7),
+    (8, 8, 256, 700, 64, -1, 47.5, 39.7, 13.7),
+    (16, 32, 20, 700, 64, -1, 35.7, 38.2, 48.5),
+    (1, 2, 9, 131072, 128, -1, 30.6, 51.3, 44.8),
+    (1, 2, 16, 131072, 64, -1, 24.4, 39.1, 34.9),
+    (1, 8, 20, 8192, 128, -1, 19, 19.9, 15.9),
+    (1, 8, 1024, 8192, 128, -1, 261.2, 173.6, 58.5),
+    (8, 8, 20, 4096, 128, -1, 36.5, 35.8, 33.4),
+    (8, 8, 64, 4096, 128, -1, 78, 56.6, 34.4),
+    (8, 8, 256, 4096, 128, -1, 267.9, 183.5, 52),
+    (8, 32, 16, 2048, 128, -1, 46.5, 39, 55),
+    (2, 8, 16, 32768, 128, -1, 46.9, 40.7, 49.7),
+    (1, 8, 16, 8192, 128, -1, 18.1, 23.4, 15.8),
+    (8, 8, 64, 2048, 64, -1, 31.9, 26.7, 17.7),
+    (16, 4, 20, 8192, 128, 2048, 26.4, 27.7, 27.3),
+    (8, 8, 512, 8192, 128, 16, 43.4, 43.2, 21.3),
+    (1, 8, 512, 8192, 64, 64, 9.5, 7.4, 10.9),
+    (64, 8, 20, 8192, 128, 128, 29, 37.9, 41.3),
+    (8, 8, 64, 8192, 128, 100, 12.3, 14.3, 10.1),
+]
+
+
+@pytest.fixture(scope="module")
+def rule(tmp_path_factory):
+    import ctypes
+    import subprocess
+    at = tmp_path_factory.mktemp("rule")
+    (at / "rule.cc").write_text("""
+        #include "fa_kv4_rule.h"
+        extern "C" int choose(int B, int H_kv, long long R, int N_q, int d, long long keys, int window, int sms, int *splits) {
+            const fa::kv4::Choice c = fa::kv4::choose(B, H_kv, R, N_q, d, keys, window, sms);
+            *splits = c.splits;
+            return c.many ? 128 : c.rows_a_block;
+        }""")
+    csrc = os.path.join(os.path.dirname(binding.__file__), "csrc")
+    subprocess.run(["g++", "-O1", "-Wall", "-Werror", "-std=c++17", "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error",
+                    "-shared", "-fPIC", "-I", csrc, "-o", str(at / "rule.so"), str(at / "rule.cc")], check=True)
+    fn = ctypes.CDLL(str(at / "rule.so")).choose
+    i32, i64 = ctypes.c_int, ctypes.c_longlong
+    fn.argtypes = [i32, i32, i64, i32, i32, i64, i32, i32, ctypes.POINTER(i32)]
+
+    def choose(B, H_kv, R, N_q, d, keys, window=-1, sms=148):
+        splits = i32()
+        return fn(B, H_kv, R, N_q, d, keys, window, sms, ctypes.byref(splits)), splits.value
+    return choose
+
+
+@pytest.mark.parametrize("B,H_kv,R,keys,d,window,us8,us16,many", MEASURED)
+def test_the_choice_of_a_kernel_is_near_the_quickest(rule, B, H_kv, R, keys, d, window, us8, us16, many):
+    kind, splits = rule(B, H_kv, R, R, d, -(-keys // 64) * 64, window)
+    us = {8: us8, 16: us16, 128: many}
+    if R <= 16:
+        us.pop(128)
+    assert us[kind] <= 1.3 * min(us.values())
+    assert 1 <= splits <= max(1, 148 // (-(-R // 128) * B * H_kv))
+
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,window", SIXTEEN_ROWS)
+def test_calls_with_sixteen_rows_a_block(rule, B, H, H_kv, N, d, page, maxp, window):
+    assert rule(B, H_kv, H // H_kv * N, N, d, page * maxp, window)[0] == 16      # what the GPU tests of these rely on
+
+
+def test_the_choice_of_a_kernel_at_the_ends_of_what_it_is_given(rule):
+    for B in (1, 65535):
+        for H_kv in (1, 65535):
+            for R in (1, 8, 9, 17, 1 << 30):
+                for keys in (0, 16, 1 << 30):
+                    for window in (-1, 0, 1 << 30):
+                        for d in (64, 128):
+                            kind, splits = rule(B, H_kv, R, R, d, keys, window)
+                            assert kind in (8, 16, 128) and 1 <= splits <= 148
+                            assert kind != 128 or R > 16
+                            assert splits == 1 or B * H_kv * R <= 148 * 128
 
 
 # ---------------------------------------------------------------- refusals
