@@ -40,6 +40,10 @@ __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Where a position of a sequence lives: its page and the token in it.  Tokens are counted
 // in 16-token tiles, the grain at which the attention kernel loads.
 struct Paging {
