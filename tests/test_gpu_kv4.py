@@ -870,6 +870,53 @@ def test_bad_pages_touch_no_other_page():
         assert np.array_equal(to_host_f64(got), want)
 
 
+def test_captured_calls_on_two_streams_that_fork_and_join():
+    """K and V are made on a side stream, written there, and attended on another: each call has one or
+    two predecessors of unlike kinds in the graph."""
+    import torch
+    from io_aware_exact_24_b200 import fa_fwd_kv4, fa_fwd_kv4_workspace_size, fa_kv4_append, fa_kv4_read
+    B, H, H_kv, N, d, page, maxp, n = 2, 8, 2, 5, 128, 16, 20, 300
+    c = filled(B, H_kv, page, d, maxp, [n, n], 161)
+    src = [tokens(B, H_kv, N, d, 162 + i)[0] for i in range(3)]
+    bits = [normal_bf16((B, H, N, d), 170 + i, 0) for i in range(3)]
+    k, v = (torch.empty_like(x) for x in src[0])
+    q_src = [to_device_bf16(b) for b in bits]
+    q, lens = torch.empty_like(q_src[0]), ints([n, n])
+    feed = [x.clone() for x in (*src[0], q_src[0])]
+    k1, v1 = torch.empty_like(k), torch.empty_like(v)
+    o, lse = torch.empty_like(q), torch.empty((B, H, N), dtype=torch.float32, device="cuda")
+    size = fa_fwd_kv4_workspace_size(B, H, H_kv, N, d)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            k.copy_(feed[0])
+            v.copy_(feed[1])
+            fa_kv4_append(k, v, *c.buffers, c.d_table, lens, None, B, H_kv, N, *c.sizes)
+            fa_kv4_read(*c.buffers, c.d_table, lens, ints_first, k1, v1, B, H_kv, N, *c.sizes)
+        torch.mul(feed[2], 1.0, out=q)
+        main.wait_stream(side)
+        fa_fwd_kv4(q, *c.buffers, c.d_table, lens, None, o, lse, B, H, H_kv, N, *c.sizes, 0.1, True, -1, ws, size)
+    ints_first = ints([n - N] * B)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in (1, 2, 0, 1):
+        for f, x in zip(feed, (*src[turn], q_src[turn])):
+            f.copy_(x)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, x in ((k1, src[turn][0]), (v1, src[turn][1])):
+            assert np.array_equal(to_host_f64(got), kv4.values(*kv4.quantise(to_host_f64(x))))
+        check(c, bits[turn], [n, n], None, 0.1, True, -1, o, lse, heads=[0, H - 1], what=str(turn))
+
+
 # ---------------------------------------------------------------- waits that run out
 
 @pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,key_lens", [
