@@ -21,12 +21,12 @@
 // What bounds it: a token and head is 144 bytes at d = 128, and at the rate at which memory
 // delivers them an SM has to take in 44 codes a cycle.  Dequantising 8 of them is 12
 // instructions of two issue cycles each, so the arithmetic, not the memory, is what a long
-// cache waits for: 4 x 32 heads on 16384 keys of 128 channels take 74 us, 4.1 TB/s, where the
-// copies alone take 57 and the arithmetic alone 72; without the FMAs of the dequantisation
-// 62, without all of it 48, without the MMAs 65.  Keeping 8, 12 or 16 warps to an SM (255,
-// 168, 128 registers) makes no difference.  A short call is a chain of latencies: lengths,
-// page, codes, a tile (0.8 us alone), the exchange, the arrival and the merge, 7.9 us for 8
-// heads on 700 keys.
+// cache waits for: 4 x 32 heads on 16384 keys of 128 channels take 75 us, 4.0 TB/s.  Of an
+// earlier 74 the copies alone took 57 and the arithmetic alone 72; without the FMAs of the
+// dequantisation it was 62, without all of it 48, without the MMAs 65.  Keeping 8, 12 or 16 warps
+// to an SM (255, 168, 128 registers) made no difference.  A short call is a chain of latencies:
+// lengths, page, codes, a tile (0.8 us alone), the exchange, the arrival and the merge, 8.4 us for
+// 8 heads on 700 keys.
 #pragma once
 
 #include <type_traits>

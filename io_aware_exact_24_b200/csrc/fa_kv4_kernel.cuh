@@ -31,7 +31,7 @@ constexpr uint32_t kScaleNone = 0x7a80;          // bf16 bits of 2^118: the magn
 
 // Every kernel here begins with this: the next kernel of the stream may be set up from now on
 // (where it allows that), and the memory of the kernels before is complete.  For calls one after
-// another on a stream it hides the setup: 8 heads on 700 keys 10.3 -> 8.1 us a call.
+// another on a stream it hides the setup: 8 heads on 700 keys 10.3 -> 8.1 us, as first built.
 // A block may thus be on its SM while the kernels before it still write what it will read, so
 // memory is not read-only for its lifetime: no load here may take the non-coherent path (no
 // __ldg, no __restrict__).  What those kernels write (codes, scales, q, k, v, parts) is loaded past L1.

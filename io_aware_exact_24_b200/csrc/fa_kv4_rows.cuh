@@ -21,13 +21,13 @@
 // zeros and noted in a mask per tile, and the softmax threads, which know what their row sees,
 // make the group's channels NaN at the end.
 //
-// What bounds it: 2 x 32 heads (8 of keys), 512 queries, 8000 keys take 172 us, 756 TFLOP/s;
-// the products alone are 78 us at the rate of a large one.  256 blocks are 1.73 waves, so the
-// SMs are idle for 14 % of it.  Else no unit is full (tensor pipe 43 % of the cycles, ALU 44,
+// What bounds it: 2 x 32 heads (8 of keys), 512 queries, 8000 keys take 174 us, 746 TFLOP/s (137
+// us at d = 64); the products alone are 78 us at the rate of a large one.  256 blocks are 1.73
+// waves, so the SMs are idle for 14 % of it.  Else no unit is full (tensor pipe 43 % of the cycles, ALU 44,
 // exponentials 42, issue 54): a tile takes a CTA 1.25 us, in which the makers turn 32768 codes
 // into 64 KB of operands, the eight softmax warps take 128 x 128 scores, and each waits for the
 // other, since shared memory and TMEM hold two tiles.  A short call is launch, setup, tiles,
-// epilogue and join: 8 x 128 rows on 700 keys, 12.5 us.
+// epilogue and join: 8 x 128 rows on 700 keys, 13.2 us.
 #pragma once
 
 #include <type_traits>
