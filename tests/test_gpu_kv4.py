@@ -1079,3 +1079,42 @@ def test_sixteen_rows_a_block(B, H, H_kv, N, d, page, maxp, window):
     c.d_table.copy_(ints(table))
     o, lse, _ = run_kv4(c, q, key_lens, None, 0.1, True, window)
     check(c, bits, key_lens, None, 0.1, True, window, o, lse, heads=[0, H - 1], what="missing pages")
+
+
+# ---------------------------------------------------------------- padding and shared pages
+
+@pytest.mark.parametrize("H,H_kv,N", [(4, 2, 3), (2, 1, 40), (16, 16, 150)])
+@pytest.mark.parametrize("fill", [0x7FC0, 0x7F80, 0xFF7F])
+def test_padding_may_hold_anything_and_sequences_may_share_pages(H, H_kv, N, fill):
+    """Tokens and queries behind a sequence's own are NaN, infinite or huge; the sequences after the
+    first continue its pages (a common prefix), and one is the same as another."""
+    import torch
+    B, d, page, maxp, prefix = 4, 128, 16, 24, 160
+    new = [N, N // 2, 1, 0]
+    lens = [prefix + n for n in new]
+    own = -(-N // page)
+    table = np.full((B, maxp), -1)
+    table[:, :prefix // page] = np.arange(prefix // page)[::-1]
+    for b in range(B):
+        table[b, prefix // page:prefix // page + own] = prefix // page + b * own + np.arange(own)
+    c = Cache(prefix // page + B * own, H_kv, page, d, maxp, table)
+    (k0, v0), _ = tokens(1, H_kv, prefix, d, 181)
+    c.append(k0, v0, [prefix])                                # through the first sequence's pages
+    (k, v), _ = tokens(B, H_kv, N, d, 182)
+    bits = normal_bf16((B, H, N, d), 183, 0)
+    for b in range(B):
+        for x in (k, v):
+            x[b, :, new[b]:] = bf16_of([fill])[0]
+        bits[b, :, new[b]:] = fill
+    c.append(k, v, lens, new)
+    for causal, window in ((True, -1), (False, -1), (True, 30)):
+        o, lse, guards = run_kv4(c, to_device_bf16(bits), lens, new, 0.1, causal, window)
+        assert guards and torch.isfinite(o.float()).all()
+        clean = np.where(np.arange(N)[None, None, :, None] < np.array(new)[:, None, None, None], bits, 0).astype(np.uint16)
+        check(c, clean, lens, new, 0.1, causal, window, o, lse, heads=[0, H - 1], what=str((causal, window)))
+    # the same sequence twice: the same answers
+    c.table[1], same = table[0], to_device_bf16(bits)
+    c.d_table.copy_(ints(c.table))
+    same[1] = same[0]
+    o, lse, _ = run_kv4(c, same, [lens[0], lens[0], *lens[2:]], [new[0], new[0], *new[2:]], 0.1, True, -1)
+    assert torch.equal(o[0].view(torch.int16), o[1].view(torch.int16)) and torch.equal(lse[0], lse[1])
