@@ -473,9 +473,10 @@ FA_API int fa_kv4_read(const void *k_codes, const void *k_scales, const void *v_
  *              share a workspace must be ordered (one stream, or events); captured calls
  *              may be replayed, and graphs that are ordered may share one.
  * K and V of a key that a query does not see have no influence on it, whatever they hold.
- * Scores and sums are held in 32 bits: q k^T has to stay below 2^127, and O is finite while
- * the number of keys that a row sees times the largest |V| stays below 2^135 (2^15 keys of
- * 2^120, or any number of 2^105).  The weights of the keys are rounded to bf16 for the product
+ * Scores and sums are held in 32 bits: scale * q k^T has to stay below 2^24 in magnitude, where
+ * its own rounding is as large as what softmax tells apart, and O is finite while the number of
+ * keys that a row sees times the largest |V| stays below 2^134 (2^14 keys of 2^120, or any
+ * number of 2^104).  The weights of the keys are rounded to bf16 for the product
  * with V and O is divided by the sum of the rounded ones, as in fa_fwd: O is off by up to 2^-8
  * of the mean distance of V from O, besides its own rounding to bf16.  Weights below 2^-110 of a
  * row's largest count as zero.  The LSE comes from the weights before they are rounded.

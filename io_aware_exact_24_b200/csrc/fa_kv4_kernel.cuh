@@ -164,8 +164,9 @@ struct RowsParams {
 
 // ---------------------------------------------------------------- weights
 // Weights are 2^(score - ref - kShift), with ref the reference max of the row, which may lag by 8:
-// at most 2^-8, so that sums of n values V stay below 2^127 while n |V| stays below 2^135 (2^15
-// keys of 2^120, or any number of 2^105), and at least 2^-126, which is 2^-110 of the largest
+// at most 2^-8 (2^-7 where scores near 2^20 round the bound itself), so that sums of n values V stay
+// below 2^127 while n |V| stays below 2^134 (2^14 keys of 2^120, or any number of 2^104), and at
+// least 2^-126, which is 2^-110 of the largest
 // (smaller ones count as zero; with a shift of 24 that would be 2^-102, which shows where all other
 // keys of a row are so far below one whose value is 0).  At the other end of the format, where
 // values are multiples of 2^-110, sums of 32 bits still tell 2^-149 apart, 2^-23 of that at a

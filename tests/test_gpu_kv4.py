@@ -1045,6 +1045,36 @@ def test_tensors_that_do_not_fit_are_refused_and_nothing_is_touched():
     assert not torch.equal(codes, keep["kc"])
 
 
+@pytest.mark.parametrize("H,H_kv,N", [(1, 1, 1), (3, 1, 4), (12, 2, 2), (32, 32, 150), (4, 1, 150)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("high", [12, 18, 23.5])
+def test_large_scores_take_the_largest_key(H, H_kv, N, d, high):
+    """Scores up to 2^high: O stays within V's range, and where the largest score leads the others by
+    more than all roundings, e = (d/16 + 28) 2^-23 2^high in the natural exponent, and 30 besides, its
+    value comes back (other weights sum to less than n e^-30 < 2^-30) and the LSE is it, within e."""
+    n, page = 700, 32
+    c = filled(1, H_kv, page, d, 22, [n], 191)
+    bits = normal_bf16((1, H, N, d), 192, 0)
+    q = bf16_bits_to_f32(bits).astype(np.float64)
+    kk, vv, _ = c.positions(0, n)
+    raw = np.stack([q[0, h] @ kk[h // (H // H_kv)].T for h in range(H)])               # [H, N, n]
+    mag = np.stack([np.abs(q[0, h]) @ np.abs(kk[h // (H // H_kv)]).T for h in range(H)]).max()
+    scale = float(np.float32(2.0 ** high / mag))
+    o, lse, guards = run_kv4(c, to_device_bf16(bits), [n], None, scale, False, -1)
+    assert guards
+    o, lse = to_host_f64(o)[0], lse.cpu().numpy().astype(np.float64)[0]
+    s = np.sort(scale * raw, -1)
+    e = (d / 16 + 28) * 2.0 ** -23 * 2.0 ** high
+    clear = s[..., -1] - s[..., -2] > 2 * e + 30
+    assert clear.mean() > 0.5 or clear.size < 100
+    for h in range(H):
+        v = vv[h // (H // H_kv)]
+        assert (np.abs(o[h]) <= np.abs(v).max(0) * (1 + 2.0 ** -7)).all()              # P's rounding and O's
+        best = v[raw[h].argmax(-1)]
+        assert (np.abs(o[h] - best)[clear[h]] <= 2.0 ** -8 * np.abs(best)[clear[h]] + 2.0 ** -25).all()
+        assert (np.abs(lse[h] - s[h, :, -1])[clear[h]] <= e + 2.0 ** -20 * 2.0 ** high).all()
+
+
 # ---------------------------------------------------------------- sixteen rows a block
 
 @pytest.mark.parametrize("B,H,H_kv,N,d,page,maxp,window", SIXTEEN_ROWS)
